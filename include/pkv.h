@@ -51,7 +51,8 @@ typedef enum {
   PKV_EUNSUPPORTED = -4  /* valid but outside what the kernels handle        */
 } pkv_status;
 
-typedef enum { PKV_FP32 = 0, PKV_BF16 = 1 } pkv_dtype;
+/* PKV_FP16 is a type of keys, values and queries; logits are fp32 or bf16. */
+typedef enum { PKV_FP32 = 0, PKV_BF16 = 1, PKV_FP16 = 2 } pkv_dtype;
 
 /* Bits of the device status word. */
 #define PKV_ST_NONFINITE 1     /* NaN in a row, or +inf in a sampled row       */
@@ -401,6 +402,193 @@ int pkv_philox_uniforms(uint64_t seed, uint64_t offset, int B, float* uniform,
 int pkv_check_free_list(const int32_t* free_slots, int64_t free_count, int page_size,
                         int64_t num_pages, int64_t cache_pages, uint32_t* bitmap,
                         int64_t bitmap_words, int32_t* result, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged KV cache, held in 8 bits: between the step's preparation
+ * (pkv_prepare_step's positions and out_loc) and the model's logits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_kv_cache -- one layer's keys and values.  A host struct of device
+ * pointers and sizes; the caller keeps it and passes its address.
+ *
+ * Token location `loc` (what page tables hold) is slot loc % page_size of
+ * page loc / page_size.  The element of (page, slot, head, i) is at
+ *   k[page * page_stride + slot * token_stride + head * head_stride + i]
+ * (v alike; the strides are in elements, and an element is one byte), an e4m3
+ * code: 4 exponent and 3 mantissa bits, largest value 448, 0x7f / 0xff NaN.
+ * It stands for code * k_scale[page * kv_heads + head].  Scales are fp32 in
+ * [2^-64, 2^119]; pkv_append_kv writes powers of two.
+ *   Requirements: k, v 16-byte aligned; the strides multiples of 16;
+ *   head_dim a multiple of 16 in [16, PKV_MAX_HEAD_DIM]; page_size and
+ *   kv_heads >= 1; num_pages * page_size < 2^31; page_stride <= 2^40 and
+ *   num_pages * page_stride, page_size * token_stride and
+ *   kv_heads * head_stride at most 2^46.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* [num_pages, kv_heads] */
+  float* v_scale; /* [num_pages, kv_heads] */
+  int64_t num_pages;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t reserved; /* 0 */
+} pkv_kv_cache;
+
+#define PKV_MAX_HEAD_DIM 128
+
+/*
+ * pkv_append_kv -- writes a step's keys and values into the cache at the
+ * locations out_loc (pkv_prepare_step's), rotating q and k by position.
+ *
+ * For packed token j < n (n = min(n_tokens, *total_tokens) when total_tokens
+ * is given):
+ *   k' = R(positions[j]) k[j],  q_out[j] = R(positions[j]) q[j],
+ * where R turns pair i < rot_dim / 2 by the angle whose cosine and sine are
+ * cos_sin[p, i] and cos_sin[p, rot_dim / 2 + i]: (a, b) becomes
+ * (a cos - b sin, b cos + a sin).  A head's pair i is its elements
+ * (i, rot_dim / 2 + i), or (2i, 2i + 1) with `interleaved`; elements from
+ * rot_dim on stay.  Then k' and v[j] become e4m3 codes of page
+ * out_loc[j] / page_size under one scale per (page, head).  With a the largest
+ * finite magnitude among the call's tokens of that page and head, and
+ * s = 2^e, e the least integer in [-64, 119] with a <= 448 * 2^e:
+ *   - a page whose slot 0 is among the call's tokens starts anew: its scale
+ *     is s;
+ *   - a page that was begun earlier takes max(scale, s); if that is larger
+ *     than its scale, the codes in the slots before the call's first are
+ *     rounded again to it.
+ * Codes are rounded to nearest even and limited to +-448; a NaN stays a NaN
+ * and PKV_ST_NONFINITE is set for NaN and infinities.  Arithmetic is fp32;
+ * a page's result does not depend on how calls on other pages are split.
+ *
+ * Tokens of one page have to be next to one another in the packed order (as
+ * pkv_prepare_step packs them), at ascending locations, and no page may be
+ * appended to for two requests at once.  A token whose out_loc lies outside
+ * the cache sets PKV_ST_ROW_OOB, one whose position lies outside
+ * [0, max_pos) (with rot_dim > 0) sets PKV_ST_COL_OOB; either is skipped
+ * (nothing of it is written, q_out included).
+ *   k, v  [n_tokens, kv_heads, head_dim] of type dt (bf16 or fp16), element
+ *         (j, h, i) at j * token_stride + h * head_stride + i, in elements;
+ *   q, q_out  the same with q_heads and their own strides, or q NULL: no
+ *         queries (q_heads 0).  q_out may be q itself (same strides).
+ *   positions, out_loc [n_tokens] int32; total_tokens device int64 or NULL;
+ *   cos_sin [max_pos, rot_dim] fp32, or NULL with rot_dim 0: no rotation
+ *         (q is then copied to q_out); rot_dim a multiple of 8, at most
+ *         head_dim; 16-byte aligned;
+ *   status device int32 or NULL.
+ * Errors: PKV_EINVAL (NULL pointer, bad cache, dtype, sizes, rot_dim, or
+ * strides; pointers and strides must keep every row 16-byte aligned),
+ * PKV_ECUDA.  n_tokens == 0 is a no-op.
+ */
+int pkv_append_kv(const pkv_kv_cache* cache, const void* k, int64_t k_token_stride,
+                  int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                  int64_t v_head_stride, pkv_dtype dt, int64_t n_tokens,
+                  const int64_t* total_tokens, const int32_t* positions, const int32_t* out_loc,
+                  const float* cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                  const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                  void* q_out, int64_t o_token_stride, int64_t o_head_stride, int32_t* status,
+                  pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention -- attention of a step's query tokens over the cache.
+ *
+ * Request i has the query tokens at positions [cached_len[i], device_len[i]),
+ * packed in batch order (as pkv_prepare_step packs them), and its keys and
+ * values at the locations page_table[table_idx[i], 0 .. device_len[i]).  The
+ * query at position p sees position t when
+ *   max(kv_begin[i], p - window + 1) <= t <= p
+ * (no window when window <= 0; kv_begin NULL is 0).  Query head h reads
+ * cache head h / (q_heads / kv_heads).  With s_t = sm_scale * (q . k_t):
+ *   out = sum_t exp(s_t - lse) v_t,   lse = ln sum_t exp(s_t)
+ * over the positions seen; a query that sees none gets zeros and -inf.  What
+ * lies in places that a query does not see never reaches it.  The softmax
+ * runs in fp32; products are of the query, the codes and weights of at least
+ * 8 significant bits, accumulated in fp32.  Sums are joined in a fixed order:
+ * equal calls give equal bits.
+ *
+ * max_q_len is the host's bound on a request's query tokens.  A request with
+ * more sets PKV_ST_TOKEN_CAP; one with a table row outside the table sets
+ * PKV_ST_ROW_OOB; one with cached_len < 0 or device_len > pt_cols sets
+ * PKV_ST_COL_OOB.  Their rows get zeros and -inf (rows past n_tokens are not
+ * written; PKV_ST_TOKEN_CAP is set when the lengths ask for more).  A
+ * location outside the cache sets PKV_ST_ROW_OOB and reads as a zero key and
+ * a zero value.
+ *   q [n_tokens, q_heads, head_dim] of type dt (bf16 or fp16), out alike,
+ *   with token and head strides in elements; lse [n_tokens, q_heads] fp32 or
+ *   NULL; cached_len, device_len, table_idx [B] int32; kv_begin [B] int32 or
+ *   NULL; page_table [pt_rows, pt_cols] int32; status device int32 or NULL;
+ *   workspace of pkv_paged_attention_workspace_bytes(...) bytes, 16-byte
+ *   aligned, zeroed before its first use; every call leaves it ready for the
+ *   next on the same stream, and no two calls that may overlap share one.
+ * Errors: PKV_EINVAL (NULL pointer, bad cache, dtype, sizes, B outside
+ * [0, PKV_MAX_FILL_BATCH], q_heads not a multiple of kv_heads, strides or
+ * pointers that leave a row unaligned to 16 bytes, sm_scale not finite,
+ * workspace missing, too small or unaligned), PKV_ECUDA.  B == 0 or
+ * n_tokens == 0 is a no-op.
+ */
+int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, int q_heads, pkv_dtype dt, int64_t n_tokens,
+                        void* out, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                        const int32_t* cached_len, const int32_t* device_len,
+                        const int32_t* table_idx, const int32_t* kv_begin, int B, int max_q_len,
+                        const int32_t* page_table, int64_t pt_rows, int64_t pt_cols,
+                        float sm_scale, int window, int32_t* status, void* workspace,
+                        size_t workspace_bytes, pkv_stream_t stream);
+
+/* Device bytes of pkv_paged_attention's workspace (0 for invalid sizes). */
+size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_len, int q_heads,
+                                           int kv_heads, int head_dim);
+
+/*
+ * pkv_adjust_logits -- what is done to a step's logits before
+ * pkv_sample_batch: penalties for repeated tokens, biases, a grammar mask.
+ *
+ * Row b's history is token_pool[table_idx[b], 0 .. device_len[b]): a prompt of
+ * prompt_len[b] tokens, then the tokens made so far.  For token v, with c its
+ * count among the tokens made:
+ *   x = logits[b, v]
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]   if v is in the history
+ *   x = x - frequency[b] * c - (c > 0 ? presence[b] : 0)
+ *   x = x + the biases of v, one after another in list order
+ *   x = -inf                                   if v's bit in the mask is 0
+ * in fp32, rounded once to the logits' type.  Row b's biases are the pairs
+ * (bias_ids[e], bias_values[e]), bias_ptr[b] <= e < bias_ptr[b + 1].  Bit
+ * v % 32 of mask[b * mask_stride + v / 32] is v's.  A masked place is -inf
+ * whatever was there, NaN included.  An element that no rule touches keeps
+ * its bits.
+ *
+ * `out` may be `logits` itself (same stride): then only what changes is
+ * written.  Otherwise the two must not overlap, and all B * V of out is
+ * written.  Entries of the history outside [0, V) count for nothing; a bias
+ * whose id lies outside is dropped and PKV_ST_COL_OOB set.  A row whose
+ * table_idx lies outside the pool sets PKV_ST_ROW_OOB, one with device_len
+ * outside [0, pool_cols] PKV_ST_COL_OOB, and has no history; one whose
+ * bias_ptr is not ascending within [0, n_bias] sets PKV_ST_COL_OOB and has no
+ * biases.  prompt_len is limited to [0, device_len].
+ *   logits, out [B, V] of type dt (fp32 or bf16), row strides in elements;
+ *   token_pool [pool_rows, pool_cols] int32 with table_idx, prompt_len,
+ *   device_len [B] int32, or all four NULL (no history); repetition (> 0),
+ *   presence, frequency [B] fp32, each NULL for none; bias_ptr [B + 1],
+ *   bias_ids [n_bias] int32, bias_values [n_bias] fp32, or all NULL; mask
+ *   int32 rows of ceil(V / 32) words, mask_stride apart, or NULL; status
+ *   device int32 or NULL.
+ * Errors: PKV_EINVAL (NULL logits or out, one of a group missing, sizes,
+ * strides, B outside [0, 65535], pool_cols >= 2^30), PKV_EUNSUPPORTED (V
+ * above PKV_MAX_VOCAB_*), PKV_ECUDA.  B == 0 is a no-op.
+ */
+int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dtype dt, int B, int V,
+                      void* out, int64_t out_stride, const int32_t* token_pool,
+                      int64_t pool_rows, int64_t pool_cols, const int32_t* table_idx,
+                      const int32_t* prompt_len, const int32_t* device_len,
+                      const float* repetition, const float* presence, const float* frequency,
+                      const int32_t* bias_ptr, const int32_t* bias_ids, const float* bias_values,
+                      int64_t n_bias, const int32_t* mask, int64_t mask_stride, int32_t* status,
+                      pkv_stream_t stream);
 
 #ifdef __cplusplus
 }

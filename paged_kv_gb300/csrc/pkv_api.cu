@@ -14,6 +14,7 @@
 #include <atomic>
 
 #include "../../include/pkv.h"
+#include "api_common.h"
 #include "launch_config.h"
 #include "page_kernels.h"
 #include "sample_params.h"
@@ -25,9 +26,11 @@ cudaError_t launch_sample_fp32(const SampleParams& P, const SampleConfig& c, int
                                cudaStream_t stream);
 }  // namespace pkv
 
-namespace {
+namespace pkv {
 
+namespace {
 thread_local char g_err[512] = "";
+}  // namespace
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -46,8 +49,7 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// SM count of the current device (cached per device; threads that race on
-// the first call store the same value).
+// Threads that race on the first call store the same value.
 int num_sms() {
   static std::atomic<int> cache[64] = {};
   int dev = 0;
@@ -62,15 +64,18 @@ int num_sms() {
   return n;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace pkv
 
-int64_t div_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-}  // namespace
+using pkv::aligned16;
+using pkv::cuda_fail;
+using pkv::div_ceil;
+using pkv::fail;
+using pkv::num_sms;
+using pkv::ok;
 
 extern "C" {
 
-const char* pkv_last_error(void) { return g_err; }
+const char* pkv_last_error(void) { return pkv::g_err; }
 
 int pkv_version(void) { return 310; }
 

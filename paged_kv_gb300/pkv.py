@@ -21,8 +21,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
 PKV_OK, PKV_EINVAL, PKV_ENOSPC, PKV_ECUDA, PKV_EUNSUPPORTED = 0, -1, -2, -3, -4
-PKV_FP32, PKV_BF16 = 0, 1
+PKV_FP32, PKV_BF16, PKV_FP16 = 0, 1, 2
 PKV_MAX_VOCAB_FP32, PKV_MAX_VOCAB_BF16 = 262144, 524288
+PKV_MAX_HEAD_DIM = 128
 ST_NONFINITE, ST_ALL_NEG_INF, ST_ROW_OOB, ST_COL_OOB, ST_BAD_UNIFORM, ST_NOSPC = 1, 2, 4, 8, 16, 32
 ST_TIMEOUT = 64
 ST_TOKEN_CAP = 128
@@ -84,6 +85,19 @@ def load() -> ctypes.CDLL:
                                              i64, i64, vp, vp, vp, i64, vp, vp, vp, vp]
             lib.pkv_philox_uniforms.restype = i32
             lib.pkv_philox_uniforms.argtypes = [ctypes.c_uint64, ctypes.c_uint64, i32, vp, vp]
+            f32 = ctypes.c_float
+            lib.pkv_append_kv.restype = i32
+            lib.pkv_append_kv.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp, vp, vp,
+                                          i64, i32, i32, vp, i64, i64, i32, vp, i64, i64, vp, vp]
+            lib.pkv_paged_attention_workspace_bytes.restype = sz
+            lib.pkv_paged_attention_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
+            lib.pkv_paged_attention.restype = i32
+            lib.pkv_paged_attention.argtypes = [vp, vp, i64, i64, i32, i32, i64, vp, i64, i64, vp,
+                                                vp, vp, vp, vp, i32, i32, vp, i64, i64, f32, i32,
+                                                vp, vp, sz, vp]
+            lib.pkv_adjust_logits.restype = i32
+            lib.pkv_adjust_logits.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, i64, i64, vp,
+                                              vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp]
             lib.pkv_check_free_list.restype = i32
             lib.pkv_check_free_list.argtypes = [vp, i64, i32, i64, i64, vp, i64, vp, vp]
             _lib = lib
@@ -443,3 +457,264 @@ def check_free_list(free_slots: torch.Tensor, free_count: int, page_size: int, n
         int(num_pages), int(cache_pages), _dev(bitmap, torch.int32, "bitmap"), bitmap.numel(),
         _dev(result, torch.int32, "result", 1), _stream(stream, result.device))
     _check(rc)
+
+
+# ------------------------------------------------------------------ the paged KV cache
+
+
+class _KVCacheStruct(ctypes.Structure):
+    """pkv_kv_cache of include/pkv.h."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KVCache:
+    """One layer's paged keys and values in 8 bits (pkv_kv_cache).
+
+    ``k`` and ``v`` are float8_e4m3fn [num_pages, page_size, kv_heads, head_dim]
+    with the same strides, the last of them 1 and the others multiples of 16;
+    ``k_scale`` and ``v_scale`` are contiguous fp32 [num_pages, kv_heads].  The
+    object keeps the tensors alive; it is made once and passed to every call.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if t.dtype != torch.float8_e4m3fn:
+                raise TypeError(f"{name} must be torch.float8_e4m3fn, got {t.dtype}")
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim] with unit "
+                                 "last stride")
+        pages, ps, heads, dim = k.shape
+        # The stride of a dimension of one is never used, and torch leaves any value in it.
+        strides, v_strides = ([x.stride(i) if x.shape[i] > 1 else 0 for i in range(3)]
+                              for x in (k, v))
+        if k.shape != v.shape or strides != v_strides or k.device != v.device:
+            raise ValueError("k and v must have the same shape, strides and device")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _dev(t, torch.float32, name, pages * heads)
+            if tuple(t.shape) != (pages, heads) or t.device != k.device:
+                raise ValueError(f"{name} must be [{pages}, {heads}] on {k.device}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, ps, heads, dim
+        self.device = k.device
+        self._struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                      v_scale.data_ptr(), pages, *strides, ps, heads, dim, 0)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+              device="cuda") -> "KVCache":
+        """A new cache (codes zero, scales one) in which a page's tokens lie next
+        to one another for each head, so that attention reads whole pages in one
+        piece."""
+        shape = (int(num_pages), int(kv_heads), int(page_size), int(head_dim))
+
+        def codes():
+            t = torch.zeros(shape, dtype=torch.uint8, device=device)
+            return t.view(torch.float8_e4m3fn).permute(0, 2, 1, 3)
+
+        def scales():
+            return torch.ones(shape[:2], dtype=torch.float32, device=device)
+
+        return cls(codes(), codes(), scales(), scales())
+
+
+def _half_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return PKV_BF16
+    if t.dtype == torch.float16:
+        return PKV_FP16
+    raise TypeError(f"{name} dtype {t.dtype} is not bf16 or fp16")
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape, name: str):
+    """(pointer, token stride, head stride) of a [tokens, heads, head_dim] CUDA tensor."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name} must have unit last stride")
+    # The stride of a dimension of one is never used, and torch leaves any value in it.
+    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+
+
+def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+              out_loc: torch.Tensor, cos_sin: Optional[torch.Tensor] = None,
+              interleaved: bool = False, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, total_tokens: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """pkv_append_kv: write the packed tokens' ``k`` and ``v`` [n, kv_heads, head_dim]
+    into ``cache`` at ``out_loc``, with k and ``q`` [n, q_heads, head_dim] rotated by
+    ``positions`` under ``cos_sin`` [max_pos, rot_dim] (cosines, then sines; None: no
+    rotation).  Returns the rotated queries (``q_out``, allocated here if not given;
+    None without ``q``).  See include/pkv.h."""
+    lib = load()
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    n = k.shape[0]
+    shape = (n, cache.kv_heads, cache.head_dim)
+    code = _half_code(k, "k")
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+    q_args = (None, 0, 0, 0, None, 0, 0)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_shape = (n, q.shape[1], cache.head_dim)
+        q_args = (*_rows(q, k.dtype, q_shape, "q"), q.shape[1],
+                  *_rows(q_out, k.dtype, q_shape, "q_out"))
+    elif q_out is not None:
+        raise ValueError("q_out given without q")
+    rc = lib.pkv_append_kv(
+        cache._ref, *_rows(k, k.dtype, shape, "k"), *_rows(v, k.dtype, shape, "v"), code, n,
+        _dev(total_tokens, torch.int64, "total_tokens", 1),
+        _dev(positions, torch.int32, "positions", n), _dev(out_loc, torch.int32, "out_loc", n),
+        _dev(cos_sin, torch.float32, "cos_sin"), max_pos, rot, int(interleaved), *q_args,
+        _dev(status, torch.int32, "status", 1), _stream(stream, cache.device))
+    _check(rc)
+    return q_out
+
+
+_attention_workspaces = {}
+
+
+def paged_attention_workspace_bytes(B: int, n_tokens: int, max_q_len: int, q_heads: int,
+                                    kv_heads: int, head_dim: int) -> int:
+    """pkv_paged_attention_workspace_bytes."""
+    return int(load().pkv_paged_attention_workspace_bytes(int(B), int(n_tokens), int(max_q_len),
+                                                          int(q_heads), int(kv_heads),
+                                                          int(head_dim)))
+
+
+def _attention_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
+    """As ``_workspace``: one zero-initialised buffer per device, for one stream at a time."""
+    ws = _attention_workspaces.get(device.index)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _attention_workspaces[device.index] = ws
+    return ws
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, cached_len: torch.Tensor,
+                    device_len: torch.Tensor, table_idx: torch.Tensor, page_table: torch.Tensor,
+                    max_q_len: int, sm_scale: Optional[float] = None, window: int = 0,
+                    kv_begin: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pkv_paged_attention: causal attention of the packed queries ``q`` [n, q_heads,
+    head_dim] (request i's are the positions [cached_len[i], device_len[i])) over
+    ``cache``.  ``max_q_len`` bounds a request's query tokens (1 for a decode step);
+    ``sm_scale`` defaults to head_dim ** -0.5.  ``workspace`` (zeroed uint8, one per
+    stream) defaults to a buffer cached per device.  Returns ``out`` (allocated here if
+    not given); ``lse`` [n, q_heads] fp32 receives the log-sum-exp if given.  See
+    include/pkv.h."""
+    lib = load()
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D")
+    code = _half_code(q, "q")
+    n, heads, dim = q.shape
+    shape = (n, heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    B = cached_len.numel()
+    max_q_len = int(max_q_len)
+    need = lib.pkv_paged_attention_workspace_bytes(B, n, max_q_len, heads, cache.kv_heads, dim)
+    if workspace is None:
+        workspace = _attention_workspace(cache.device, need)
+    elif workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+    rc = lib.pkv_paged_attention(
+        cache._ref, *_rows(q, q.dtype, shape, "q"), heads, code, n,
+        *_rows(out, q.dtype, shape, "out"), _dev(lse, torch.float32, "lse", n * heads),
+        _dev(cached_len, torch.int32, "cached_len", B),
+        _dev(device_len, torch.int32, "device_len", B),
+        _dev(table_idx, torch.int32, "table_idx", B), _dev(kv_begin, torch.int32, "kv_begin", B),
+        B, max_q_len, _dev(page_table, torch.int32, "page_table"), page_table.shape[0],
+        page_table.shape[1], dim ** -0.5 if sm_scale is None else float(sm_scale), int(window),
+        _dev(status, torch.int32, "status", 1), workspace.data_ptr(), workspace.numel(),
+        _stream(stream, cache.device))
+    _check(rc)
+    return out
+
+
+def adjust_logits(logits: torch.Tensor, out: Optional[torch.Tensor] = None,
+                  token_pool: Optional[torch.Tensor] = None,
+                  table_idx: Optional[torch.Tensor] = None,
+                  prompt_len: Optional[torch.Tensor] = None,
+                  device_len: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None,
+                  bias_ptr: Optional[torch.Tensor] = None,
+                  bias_ids: Optional[torch.Tensor] = None,
+                  bias_values: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """pkv_adjust_logits: repetition, presence and frequency penalties over each row's
+    history in ``token_pool``, then sparse biases, then a grammar bit mask
+    ([B, ceil(V / 32)] int32), into ``out`` (None: in place).  Returns it.  See
+    include/pkv.h."""
+    lib = load()
+    if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
+        raise ValueError("logits must be a 2-D CUDA tensor with unit column stride")
+    if logits.dtype == torch.bfloat16:
+        dcode = PKV_BF16
+    elif logits.dtype == torch.float32:
+        dcode = PKV_FP32
+    else:
+        raise TypeError(f"logits dtype {logits.dtype} is not fp32 or bf16")
+    B, V = logits.shape
+    if out is None:
+        out = logits
+    elif (out.dim() != 2 or not out.is_cuda or out.dtype != logits.dtype
+          or out.shape != logits.shape or out.stride(1) != 1):
+        raise ValueError("out must be a CUDA tensor of the logits' shape and dtype with unit "
+                         "column stride")
+    pool_rows = pool_cols = 0
+    if token_pool is not None:
+        if token_pool.dim() != 2:
+            raise ValueError("token_pool must be 2-D")
+        pool_rows, pool_cols = token_pool.shape
+    n_bias = 0
+    if bias_ids is not None:
+        n_bias = bias_ids.numel()
+    mask_stride = 0
+    if mask is not None:
+        if (mask.dim() != 2 or not mask.is_cuda or mask.dtype != torch.int32
+                or mask.stride(1) != 1 or mask.shape[0] < B or mask.shape[1] < (V + 31) // 32):
+            raise ValueError(f"mask must be a CUDA int32 tensor [{B}, {(V + 31) // 32}] with unit "
+                             "column stride")
+        mask_stride = mask.stride(0)
+    rc = lib.pkv_adjust_logits(
+        logits.data_ptr(), logits.stride(0), dcode, B, V, out.data_ptr(), out.stride(0),
+        _dev(token_pool, torch.int32, "token_pool"), pool_rows, pool_cols,
+        _dev(table_idx, torch.int32, "table_idx", B), _dev(prompt_len, torch.int32, "prompt_len", B),
+        _dev(device_len, torch.int32, "device_len", B),
+        _dev(repetition, torch.float32, "repetition", B),
+        _dev(presence, torch.float32, "presence", B),
+        _dev(frequency, torch.float32, "frequency", B),
+        _dev(bias_ptr, torch.int32, "bias_ptr", B + 1), _dev(bias_ids, torch.int32, "bias_ids"),
+        _dev(bias_values, torch.float32, "bias_values", n_bias), n_bias,
+        mask.data_ptr() if mask is not None else None, mask_stride,
+        _dev(status, torch.int32, "status", 1), _stream(stream, logits.device))
+    _check(rc)
+    return out
