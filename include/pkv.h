@@ -569,7 +569,9 @@ size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_le
  * table_idx lies outside the pool sets PKV_ST_ROW_OOB, one with device_len
  * outside [0, pool_cols] PKV_ST_COL_OOB, and has no history; one whose
  * bias_ptr is not ascending within [0, n_bias] sets PKV_ST_COL_OOB and has no
- * biases.  prompt_len is limited to [0, device_len].
+ * biases.  prompt_len is limited to [0, device_len].  Bias lists are meant to
+ * be sparse: beyond some hundreds of entries a row their cost grows with the
+ * square of the list.
  *   logits, out [B, V] of type dt (fp32 or bf16), row strides in elements;
  *   token_pool [pool_rows, pool_cols] int32 with table_idx, prompt_len,
  *   device_len [B] int32, or all four NULL (no history); repetition (> 0),

@@ -2,21 +2,23 @@
 //
 // A CTA owns one slice of one row's vocabulary and a shared-memory cell for
 // every token of it.  It scans the row's whole history (a few KB to some tens
-// of KB, from L2 after the first slice) and counts the tokens that fall in
-// its slice: a prompt token sets the cell's "seen" bit, a made one adds 1; a
-// bias sets its bit.  Integer sums, so the order of the atomics leaves no
-// trace.  Then:
-//   * out of place: the slice streams through once, 16 bytes a thread; an
-//     element whose cell is zero and whose mask bit is set is copied;
-//   * in place: only tokens with a cell are read and written (the first
-//     thread to take a cell's content applies it), then masked places are
+// of KB, from L2 after the row's first slice) and counts the tokens that fall
+// in its slice: a prompt token sets the cell's "seen" bit, a made one adds 1.
+// Integer sums, so the order of the atomics leaves no trace.  Then:
+//   * out of place: the slice streams through once, kUnroll 16-byte loads a
+//     thread in flight; an element whose cell is zero and whose mask bit is
+//     set is copied, and logits under a zero mask are not even read.  The few
+//     biased tokens are computed again from the logits and overwritten;
+//   * in place: only tokens with a cell or a bias are read and written (the
+//     thread that takes a cell's content applies it), then masked places are
 //     filled with -inf.
-// Biases are added by searching the row's list for the element's token, in
-// list order: only elements with a bias do, and the sum has one order.
+// The row's biases that fall in the slice are gathered in list order; the
+// thread of a token's first bias adds all of them, so the sum has one order.
 //
-// Bound: bytes (out of place: one read and one write of the logits).  Cells
-// are 16 bits where a count fits 14 bits (token pools of up to 16383
-// columns), 32 bits otherwise.
+// Cells are 16 bits where the row's made tokens number at most 16383 (a
+// 14-bit count), else 32 bits, in two passes of half a slice.
+//
+// Bound: bytes (out of place: one read and one write of the logits).
 
 #include <cuda_runtime.h>
 
@@ -36,8 +38,10 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kUnroll = 4;
 constexpr int kCellBytes = 96 * 1024;  // shared memory of the cells: two CTAs an SM
 constexpr int kMaxCount16 = 16383;
+constexpr int kBiasCap = 512;          // gathered biases of a slice
 
 struct AdjustParams {
   const void* logits;
@@ -62,10 +66,10 @@ struct AdjustParams {
 
 template <int BITS> struct CellOf;
 template <> struct CellOf<16> {
-  static constexpr uint32_t kSeen = 0x8000u, kBias = 0x4000u, kCount = 0x3fffu;
+  static constexpr uint32_t kSeen = 0x8000u, kCount = 0x3fffu;
 };
 template <> struct CellOf<32> {
-  static constexpr uint32_t kSeen = 0x80000000u, kBias = 0x40000000u, kCount = 0x3fffffffu;
+  static constexpr uint32_t kSeen = 0x80000000u, kCount = 0x3fffffffu;
 };
 
 template <int BITS>
@@ -90,22 +94,20 @@ __device__ __forceinline__ uint32_t cell_take(uint32_t* cells, int i) {
   return (atomicAnd(cells + (i >> 1), ~(0xffffu << sh)) >> sh) & 0xffffu;
 }
 
+// One row as its CTAs see it.
 struct Row {
   float rep, pres, freq;
+  int len, prompt;
+  const int32_t* hist;
   int bias_begin, bias_end;
+  const uint32_t* mask;
 };
 
 template <int BITS>
-__device__ __forceinline__ float adjust(const AdjustParams& P, const Row& r, float x, uint32_t cell,
-                                        int v) {
-  using C = CellOf<BITS>;
-  const uint32_t count = cell & C::kCount;
-  if ((cell & ~C::kBias) != 0u) x = x > 0.0f ? x / r.rep : x * r.rep;
+__device__ __forceinline__ float penalise(const Row& r, float x, uint32_t cell) {
+  const uint32_t count = cell & CellOf<BITS>::kCount;
+  if (cell != 0u) x = x > 0.0f ? x / r.rep : x * r.rep;
   if (count != 0u) x = x - r.freq * static_cast<float>(count) - r.pres;
-  if ((cell & C::kBias) != 0u) {
-    for (int e = r.bias_begin; e < r.bias_end; ++e)
-      if (P.bias_ids[e] == v) x += P.bias_values[e];
-  }
   return x;
 }
 
@@ -114,36 +116,224 @@ __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void store_one(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ bool allowed(const Row& r, int v) {
+  return r.mask == nullptr || ((r.mask[v >> 5] >> (v & 31)) & 1u) != 0u;
+}
+
+// -inf in every element of a 16-byte vector.
+template <typename T> __device__ __forceinline__ uint32_t minus_inf_word();
+template <> __device__ __forceinline__ uint32_t minus_inf_word<float>() { return 0xff800000u; }
+template <> __device__ __forceinline__ uint32_t minus_inf_word<__nv_bfloat16>() { return 0xff80ff80u; }
+
+// The tokens [v0, v1) of one row.
 template <typename T, int BITS, bool INPLACE>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustParams P) {
+__device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T* out, int v0,
+                             int v1, uint32_t* cells, int* s_id, float* s_val, int* s_count) {
   using C = CellOf<BITS>;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int nv = v1 - v0;
+  const bool counted = r.len > 0;
+  const bool biased = r.bias_end > r.bias_begin;
+
+  // ---- cells and the slice's biases
+  if (counted) {
+    const int words = (nv * (BITS / 8) + 15) / 16;
+    for (int i = tid; i < words; i += kThreads)
+      reinterpret_cast<uint4*>(cells)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    auto note = [&](int tok, int at) {
+      const uint32_t i = static_cast<uint32_t>(tok - v0);
+      if (i >= static_cast<uint32_t>(nv)) return;
+      if (at >= r.prompt) cell_add<BITS>(cells, i, 1u);
+      else cell_or<BITS>(cells, i, C::kSeen);
+    };
+    // 16-byte loads from the first aligned entry on.
+    const int head = min(
+        r.len, static_cast<int>((4 - ((reinterpret_cast<uintptr_t>(r.hist) >> 2) & 3)) & 3));
+    const int quads = (r.len - head) >> 2;
+    if (tid < head) note(r.hist[tid], tid);
+    const int4* h4 = reinterpret_cast<const int4*>(r.hist + head);
+#pragma unroll 4
+    for (int i = tid; i < quads; i += kThreads) {
+      const int4 t = h4[i];
+      const int at = head + 4 * i;
+      note(t.x, at), note(t.y, at + 1), note(t.z, at + 2), note(t.w, at + 3);
+    }
+    const int rest = head + 4 * quads + tid;
+    if (rest < r.len) note(r.hist[rest], rest);
+  }
+  if (biased && tid >= kThreads - 32) {
+    // The last warp gathers the slice's biases in list order.
+    int n = 0;
+    for (int e0 = r.bias_begin; e0 < r.bias_end; e0 += 32) {
+      const int e = e0 + lane;
+      int id = -1;
+      if (e < r.bias_end) id = P.bias_ids[e];
+      const bool mine = id >= v0 && id < v1;
+      const unsigned m = __ballot_sync(kFull, mine);
+      const int at = n + __popc(m & ((1u << lane) - 1u));
+      if (mine && at < kBiasCap) s_id[at] = id, s_val[at] = P.bias_values[e];
+      n += __popc(m);
+    }
+    if (lane == 0) *s_count = n;
+  }
+  __syncthreads();
+
+  // Calls f(token, sum of x and its biases) in the thread of each biased
+  // token's first bias.
+  auto each_biased = [&](auto&& f) {
+    const int n = *s_count;
+    const bool gathered = n <= kBiasCap;
+    const int* ids = gathered ? s_id : P.bias_ids;
+    const float* vals = gathered ? s_val : P.bias_values;
+    const int e0 = gathered ? 0 : r.bias_begin, e1 = gathered ? n : r.bias_end;
+    for (int e = e0 + tid; e < e1; e += kThreads) {
+      const int id = ids[e];
+      if (id < v0 || id >= v1) continue;
+      bool first = true;
+      for (int k = e0; k < e && first; ++k) first = ids[k] != id;
+      if (!first) continue;
+      f(id, [&](float x) {
+        for (int k = e; k < e1; ++k)
+          if (ids[k] == id) x += vals[k];
+        return x;
+      });
+    }
+  };
+
+  if (INPLACE) {
+    if (biased) {
+      each_biased([&](int v, auto&& add) {
+        const uint32_t c = counted ? cell_take<BITS>(cells, v - v0) : 0u;
+        store_one(out + v, add(penalise<BITS>(r, load_one(out + v), c)));
+      });
+      __syncthreads();
+    }
+    for (int i = tid; i < r.len; i += kThreads) {
+      const int tok = r.hist[i];
+      const uint32_t k = static_cast<uint32_t>(tok - v0);
+      if (k >= static_cast<uint32_t>(nv) || cell_get<BITS>(cells, k) == 0u) continue;
+      const uint32_t c = cell_take<BITS>(cells, k);
+      if (c != 0u) store_one(out + tok, penalise<BITS>(r, load_one(out + tok), c));
+    }
+    if (r.mask != nullptr) {
+      __syncthreads();  // a masked place is -inf whatever was written there
+      const int w0 = v0 >> 5, w1 = (v1 + 31) >> 5;
+      for (int w = w0 + (tid >> 5); w < w1; w += kThreads / 32) {
+        const uint32_t bits = r.mask[w];
+        const int v = w * 32 + lane;
+        if (v < v1 && ((bits >> lane) & 1u) == 0u) store_one(out + v, -INFINITY);
+      }
+    }
+    return;
+  }
+
+  // ---- out of place: the slice once through
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr uint32_t kAll = (1u << kVec) - 1u;
+  const int vecs = P.vec ? nv / kVec : 0;
+  for (int i0 = tid; i0 < vecs; i0 += kThreads * kUnroll) {
+    uint4 raw[kUnroll];
+    uint32_t bits[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads, v = v0 + i * kVec;
+      bits[u] = kAll;
+      if (i < vecs && r.mask != nullptr) bits[u] = (r.mask[v >> 5] >> (v & 31)) & kAll;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < vecs && bits[u] != 0u) raw[u] = ld_stream_v4(in + v);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads, at = i * kVec;
+      if (i >= vecs) break;
+      constexpr int kWords = kVec * BITS / 32;  // of cells
+      uint32_t cw[kWords];
+      uint32_t any = 0u;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) cw[k] = counted ? cells[at * BITS / 32 + k] : 0u;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) any |= cw[k];
+      uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      if (any != 0u) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          const uint32_t c = BITS == 32 ? cw[k] : (cw[k >> 1] >> ((k & 1) * 16)) & 0xffffu;
+          if (c == 0u) continue;
+          if (sizeof(T) == 4) {
+            w[k & 3] = __float_as_uint(penalise<BITS>(r, __uint_as_float(w[k & 3]), c));
+          } else {
+            const int sh = (k & 1) * 16;
+            const float x = __uint_as_float((w[(k >> 1) & 3] >> sh) << 16);
+            const uint32_t y = __bfloat16_as_ushort(__float2bfloat16_rn(penalise<BITS>(r, x, c)));
+            w[(k >> 1) & 3] = (w[(k >> 1) & 3] & ~(0xffffu << sh)) | (y << sh);
+          }
+        }
+      }
+      if (bits[u] != kAll) {
+        const uint32_t inf = minus_inf_word<T>();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t hide;
+          if (sizeof(T) == 4) {
+            hide = (bits[u] >> k) & 1u ? 0u : 0xffffffffu;
+          } else {
+            hide = ((bits[u] >> (2 * k)) & 1u ? 0u : 0xffffu) |
+                   ((bits[u] >> (2 * k + 1)) & 1u ? 0u : 0xffff0000u);
+          }
+          w[k] = (w[k] & ~hide) | (inf & hide);
+        }
+      }
+      *reinterpret_cast<uint4*>(out + v0 + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  for (int i = vecs * kVec + tid; i < nv; i += kThreads) {
+    const int v = v0 + i;
+    T x = in[v];
+    const uint32_t c = counted ? cell_get<BITS>(cells, i) : 0u;
+    if (!allowed(r, v)) store_one(&x, -INFINITY);
+    else if (c != 0u) store_one(&x, penalise<BITS>(r, load_one(&x), c));
+    out[v] = x;
+  }
+  if (biased) {
+    __syncthreads();  // biased tokens are written over
+    each_biased([&](int v, auto&& add) {
+      const uint32_t c = counted ? cell_get<BITS>(cells, v - v0) : 0u;
+      if (allowed(r, v)) store_one(out + v, add(penalise<BITS>(r, load_one(in + v), c)));
+    });
+  }
+}
+
+template <typename T, bool INPLACE>
+__global__ void __launch_bounds__(kThreads, 2) adjust_kernel(const AdjustParams P) {
   extern __shared__ __align__(16) uint32_t cells[];
-  const int tid = threadIdx.x;
+  __shared__ int s_id[kBiasCap];
+  __shared__ float s_val[kBiasCap];
+  __shared__ int s_count;
   const int b = blockIdx.x / P.slices, sl = blockIdx.x - b * P.slices;
-  const int v0 = sl * P.slice, v1 = min(P.V, v0 + P.slice), nv = v1 - v0;
+  const int v0 = sl * P.slice, v1 = min(P.V, v0 + P.slice);
   const T* in = static_cast<const T*>(P.logits) + b * P.in_stride;
   T* out = static_cast<T*>(P.out) + b * P.out_stride;
-  const uint32_t* mask = P.mask != nullptr ? P.mask + b * P.mask_stride : nullptr;
 
   Row r;
+  r.mask = P.mask != nullptr ? P.mask + b * P.mask_stride : nullptr;
   r.rep = P.repetition != nullptr ? P.repetition[b] : 1.0f;
   r.pres = P.presence != nullptr ? P.presence[b] : 0.0f;
   r.freq = P.frequency != nullptr ? P.frequency[b] : 0.0f;
+  r.len = r.prompt = 0;
+  r.hist = nullptr;
   int bad = 0;
-  int len = 0, prompt = 0;
-  const int32_t* hist = nullptr;
   if (P.token_pool != nullptr) {
     const int64_t t = P.table_idx[b];
-    len = P.device_len[b];
+    const int len = P.device_len[b];
     if (t < 0 || t >= P.pool_rows) {
       bad |= PKV_ST_ROW_OOB;
-      len = 0;
     } else if (len < 0 || len > P.pool_cols) {
       bad |= PKV_ST_COL_OOB;
-      len = 0;
     } else {
-      hist = P.token_pool + t * P.pool_cols;
-      prompt = max(0, min(len, P.prompt_len[b]));
+      r.len = len;
+      r.hist = P.token_pool + t * P.pool_cols;
+      r.prompt = max(0, min(len, P.prompt_len[b]));
     }
   }
   r.bias_begin = r.bias_end = 0;
@@ -152,131 +342,37 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustParams P) 
     if (e0 < 0 || e1 < e0 || e1 > P.n_bias) bad |= PKV_ST_COL_OOB;
     else r.bias_begin = e0, r.bias_end = e1;
   }
-  const bool touched = len > 0 || r.bias_end > r.bias_begin;
-
-  // ---- cells
-  if (touched) {
-    const int words = (nv * (BITS / 8) + 15) / 16;
-    for (int i = tid; i < words; i += kThreads)
-      reinterpret_cast<uint4*>(cells)[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    auto note = [&](int tok, int at) {
-      const int i = tok - v0;
-      if (i < 0 || i >= nv) return;
-      if (at >= prompt) cell_add<BITS>(cells, i, 1u);
-      else cell_or<BITS>(cells, i, C::kSeen);
-    };
-    int head = 0;
-    if (len > 0) {
-      // 16-byte loads from the first aligned entry on.
-      head = min(len, static_cast<int>((4 - ((reinterpret_cast<uintptr_t>(hist) >> 2) & 3)) & 3));
-      const int quads = (len - head) >> 2;
-      if (tid < head) note(hist[tid], tid);
-      const int4* h4 = reinterpret_cast<const int4*>(hist + head);
-#pragma unroll 4
-      for (int i = tid; i < quads; i += kThreads) {
-        const int4 t = h4[i];
-        const int at = head + 4 * i;
-        note(t.x, at), note(t.y, at + 1), note(t.z, at + 2), note(t.w, at + 3);
-      }
-      const int rest = head + 4 * quads + tid;
-      if (rest < len) note(hist[rest], rest);
-    }
-    for (int e = r.bias_begin + tid; e < r.bias_end; e += kThreads) {
+  if (sl == 0 && P.status != nullptr) {
+    for (int e = r.bias_begin + threadIdx.x; e < r.bias_end; e += kThreads) {
       const int v = P.bias_ids[e];
       if (v < 0 || v >= P.V) bad |= PKV_ST_COL_OOB;
-      else if (v >= v0 && v < v1) cell_or<BITS>(cells, v - v0, C::kBias);
     }
-    __syncthreads();
+    if (bad != 0) atomicOr(P.status, bad);
   }
-  if (sl == 0 && bad != 0 && P.status != nullptr) atomicOr(P.status, bad);
-
-  if (INPLACE) {
-    auto apply = [&](int tok) {
-      const int i = tok - v0;
-      if (i < 0 || i >= nv || cell_get<BITS>(cells, i) == 0u) return;
-      const uint32_t c = cell_take<BITS>(cells, i);
-      if (c != 0u) store_one(out + tok, adjust<BITS>(P, r, load_one(out + tok), c, tok));
-    };
-    for (int i = tid; i < len; i += kThreads) apply(hist[i]);
-    for (int e = r.bias_begin + tid; e < r.bias_end; e += kThreads) apply(P.bias_ids[e]);
-    if (mask != nullptr) {
-      __syncthreads();  // a masked place is -inf whatever was written there
-      const int w0 = v0 >> 5, w1 = (v1 + 31) >> 5;
-      for (int w = w0 + (tid >> 5); w < w1; w += kThreads / 32) {
-        const uint32_t bits = mask[w];
-        const int v = w * 32 + (tid & 31);
-        if (v < v1 && ((bits >> (tid & 31)) & 1u) == 0u) store_one(out + v, -INFINITY);
-      }
-    }
-    return;
-  }
-
-  // ---- out of place: the slice once through
-  constexpr int kVec = 16 / sizeof(T);
-  if (P.vec) {
-    const int vecs = (nv + kVec - 1) / kVec;
-    for (int i = tid; i < vecs; i += kThreads) {
-      const int at = i * kVec, v = v0 + at;
-      const uint32_t bits = mask != nullptr ? mask[v >> 5] >> (v & 31) : 0xffffffffu;
-      const bool full = at + kVec <= nv;
-      uint32_t any = 0u;
-      if (touched) {
-        constexpr int kWords = kVec * BITS / 32;
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) any |= cells[at * BITS / 32 + k];
-      }
-      constexpr uint32_t kAll = (1u << kVec) - 1u;
-      if (full && any == 0u && (bits & kAll) == kAll) {
-        *reinterpret_cast<uint4*>(out + v) = ld_stream_v4(in + v);
-        continue;
-      }
-      __align__(16) T x[kVec];
-      if (full) {
-        *reinterpret_cast<uint4*>(x) = ld_stream_v4(in + v);
-      } else {
-        for (int k = 0; k < nv - at; ++k) x[k] = in[v + k];
-      }
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        const uint32_t c = touched ? cell_get<BITS>(cells, at + k) : 0u;
-        if (((bits >> k) & 1u) == 0u) store_one(x + k, -INFINITY);
-        else if (c != 0u) store_one(x + k, adjust<BITS>(P, r, load_one(x + k), c, v + k));
-      }
-      if (full) {
-        *reinterpret_cast<uint4*>(out + v) = *reinterpret_cast<const uint4*>(x);
-      } else {
-        for (int k = 0; k < nv - at; ++k) out[v + k] = x[k];
-      }
-    }
+  if (r.len - r.prompt <= kMaxCount16) {
+    adjust_range<T, 16, INPLACE>(P, r, in, out, v0, v1, cells, s_id, s_val, &s_count);
   } else {
-    for (int i = tid; i < nv; i += kThreads) {
-      const int v = v0 + i;
-      T x = in[v];
-      const uint32_t c = touched ? cell_get<BITS>(cells, i) : 0u;
-      if (mask != nullptr && ((mask[v >> 5] >> (v & 31)) & 1u) == 0u) store_one(&x, -INFINITY);
-      else if (c != 0u) store_one(&x, adjust<BITS>(P, r, load_one(&x), c, v));
-      out[v] = x;
-    }
+    const int mid = min(v1, v0 + P.slice / 2);
+    adjust_range<T, 32, INPLACE>(P, r, in, out, v0, mid, cells, s_id, s_val, &s_count);
+    __syncthreads();
+    if (mid < v1)
+      adjust_range<T, 32, INPLACE>(P, r, in, out, mid, v1, cells, s_id, s_val, &s_count);
   }
 }
 
-template <typename T, int BITS, bool INPLACE>
+template <typename T, bool INPLACE>
 cudaError_t launch(const AdjustParams& P, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0ull};
-  const auto kernel = adjust_kernel<T, BITS, INPLACE>;
+  const auto kernel = adjust_kernel<T, INPLACE>;
   const cudaError_t e = set_smem_limit_once(done, kernel, kCellBytes);
   if (e != cudaSuccess) return e;
-  const int bytes = (P.slice * (BITS / 8) + 15) / 16 * 16;
-  kernel<<<static_cast<unsigned>(P.B) * P.slices, kThreads, bytes, s>>>(P);
+  kernel<<<static_cast<unsigned>(P.B) * P.slices, kThreads, P.slice * 2, s>>>(P);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_type(const AdjustParams& P, int bits, cudaStream_t s) {
-  const bool inplace = P.logits == P.out;
-  if (bits == 16) return inplace ? launch<T, 16, true>(P, s) : launch<T, 16, false>(P, s);
-  return inplace ? launch<T, 32, true>(P, s) : launch<T, 32, false>(P, s);
+cudaError_t launch_type(const AdjustParams& P, cudaStream_t s) {
+  return P.logits == P.out ? launch<T, true>(P, s) : launch<T, false>(P, s);
 }
 
 }  // namespace
@@ -351,17 +447,17 @@ extern "C" int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dty
   P.B = B, P.V = V;
   P.vec = aligned16(logits) && aligned16(out) && (row_stride * elt) % 16 == 0 &&
           (out_stride * elt) % 16 == 0;
-  const int bits = token_pool == nullptr || pool_cols <= kMaxCount16 ? 16 : 32;
   // Slices: as few as the cells allow, but enough for two CTAs an SM; a
-  // multiple of 1024 tokens, so that mask words and vectors never straddle.
-  const int cap = kCellBytes / (bits / 8);
+  // multiple of 2048 tokens, so that no mask word or vector straddles two
+  // (or two halves of one).
+  const int cap = kCellBytes / 2;
   const int64_t want = std::max<int64_t>(div_ceil(V, cap), div_ceil(2 * num_sms(), B));
   P.slice = static_cast<int>(
-      std::min<int64_t>(cap / 1024 * 1024, div_ceil(div_ceil(V, want), 1024) * 1024));
+      std::min<int64_t>(cap / 2048 * 2048, div_ceil(div_ceil(V, want), 2048) * 2048));
   P.slices = static_cast<int>(div_ceil(V, P.slice));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dt == PKV_BF16 ? launch_type<__nv_bfloat16>(P, bits, s) : launch_type<float>(P, bits, s);
+      dt == PKV_BF16 ? launch_type<__nv_bfloat16>(P, s) : launch_type<float>(P, s);
   if (e != cudaSuccess) return cuda_fail(e, "adjust launch");
   return ok();
 }

@@ -10,8 +10,13 @@
 // result does not depend on the launch.  A head's row is spread over the lanes
 // in quads (4 elements, 8 bytes in, 4 bytes out); the rotate-half partner of
 // a quad lies a fixed number of lanes away and comes by one shuffle.  A run of
-// up to kHold tokens stays in registers between the maximum and the rounding;
-// a longer one is read a second time, from L2.
+// up to kHold tokens is loaded at once and stays in registers, unrotated,
+// between the maximum and the rounding: turning it twice costs less than the
+// registers of turned values, which would halve the warps that keep loads in
+// flight.  A longer run is read a second time, from L2.
+//
+// Bound: bytes, and with few tokens the two dependent loads (a token's place,
+// then what the place needs).
 //
 // e4m3 keeps its relative precision over 2^-6 .. 448, so a power-of-two scale
 // costs nothing against a tight one and lets a page's scale grow later
@@ -33,7 +38,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kHold = 16;    // tokens of a run held in registers
-constexpr int kQHeads = 4;   // query heads a warp rotates together
+constexpr int kQHeads = 8;   // query heads a warp rotates together
 constexpr int kMaxWindow = 16;
 constexpr int kMinExp = -64, kMaxExp = 119;
 
@@ -165,25 +170,105 @@ struct Divide {
   }
 };
 
-// One (run, head, k or v), by one warp.  j0 leads the run.
-template <typename T, bool INTER>
-__device__ __forceinline__ void append_run(const AppendParams& P, int64_t n, int64_t j0, int page,
-                                           int head, bool is_v, int lane) {
-  const pkv_kv_cache& C = P.c;
-  const int ps = C.page_size;
-  const int64_t slots = C.num_pages * ps;
-  const bool turning = !is_v && P.rot > 0;
-  const uint16_t* src = is_v ? P.v + head * P.v_hs : P.k + head * P.k_hs;
-  const int64_t ts = is_v ? P.v_ts : P.k_ts;
-  uint8_t* dst = static_cast<uint8_t*>(is_v ? C.v : C.k) + page * C.page_stride +
-                 head * C.head_stride + lane * 4;
-  float* scale = (is_v ? C.v_scale : C.k_scale) + static_cast<int64_t>(page) * C.kv_heads + head;
-  const bool live = lane * 4 < C.head_dim;
-  const float before = *scale;
+// Rounds the page's codes before slot `first` from one scale to a larger one.
+__device__ __forceinline__ void regrow(uint8_t* dst, int64_t token_stride, int first, float before,
+                                       float now, bool live) {
+  const float ratio = before / now;
+  for (int t = 0; t < first; ++t) {
+    if (live) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(dst + t * token_stride);
+      const uint32_t old = *at;
+      const float2 x = Pair<__half>::unpack(e4m3x2_to_f16x2(old));
+      const float2 y = Pair<__half>::unpack(e4m3x2_to_f16x2(old >> 16));
+      *at = e4m3x2(x.x * ratio, x.y * ratio) | (e4m3x2(y.x * ratio, y.y * ratio) << 16);
+    }
+  }
+}
 
-  // Visits the run's tokens 32 at a time: lane l holds token base + l's slot
-  // (-1: skipped) and position.  Returns how many tokens from `base` on
-  // belong to the run.
+// What one warp needs of its (page, head, k or v).
+struct Target {
+  const uint16_t* src;
+  int64_t ts;
+  uint8_t* dst;
+  float* scale;
+  bool turning, live;
+};
+
+__device__ __forceinline__ Target target(const AppendParams& P, int page, int head, bool is_v,
+                                         int lane) {
+  const pkv_kv_cache& C = P.c;
+  Target t;
+  t.src = (is_v ? P.v + head * P.v_hs : P.k + head * P.k_hs) + lane * 4;
+  t.ts = is_v ? P.v_ts : P.k_ts;
+  t.dst = static_cast<uint8_t*>(is_v ? C.v : C.k) + page * C.page_stride + head * C.head_stride +
+          lane * 4;
+  t.scale = (is_v ? C.v_scale : C.k_scale) + static_cast<int64_t>(page) * C.kv_heads + head;
+  t.turning = !is_v && P.rot > 0;
+  t.live = lane * 4 < C.head_dim;
+  return t;
+}
+
+// A run of at most kHold tokens.  Lane l holds token w0 + l's slot in the page
+// (-1: not written) and position; the run's tokens are j0 .. j0 + cnt - 1,
+// j0 = w0 + at.
+template <typename T, bool INTER>
+__device__ __forceinline__ void append_held(const AppendParams& P, const Target& D, int64_t j0,
+                                            int at, unsigned valid, int slot, int pos, int lane) {
+  if (valid == 0u) return;
+  const float before = *D.scale;
+  uint2 raw[kHold];
+#pragma unroll
+  for (int t = 0; t < kHold; ++t) {
+    raw[t] = make_uint2(0u, 0u);
+    if (((valid >> t) & 1u) != 0u && D.live)
+      raw[t] = *reinterpret_cast<const uint2*>(D.src + (j0 + t) * D.ts);
+  }
+  auto value = [&](int t) -> float4 {
+    float4 x = unpack4<T>(raw[t]);
+    if (D.turning) {
+      const Turn turn = load_turn<INTER>(P, __shfl_sync(kFull, pos, at + t), lane);
+      x = rotate<INTER>(P, x, turn, lane);
+    }
+    return x;
+  };
+  float amax = 0.0f;
+  bool fine = true;
+#pragma unroll
+  for (int t = 0; t < kHold; ++t) {
+    if ((valid >> t) & 1u) {
+      const float4 x = value(t);
+      amax = fmaxf(amax, max4(x));
+      fine = fine && finite4(x);
+    }
+  }
+  amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
+  const float want = scale_for(amax);
+  const int first = __shfl_sync(kFull, slot, at + __ffs(valid) - 1);
+  const float now = first == 0 ? want : fmaxf(before, want);
+  if (first > 0 && now != before) regrow(D.dst, P.c.token_stride, first, before, now, D.live);
+  const Divide div(now);
+#pragma unroll
+  for (int t = 0; t < kHold; ++t) {
+    if ((valid >> t) & 1u) {
+      const float4 x = value(t);
+      const int o = __shfl_sync(kFull, slot, at + t);
+      if (D.live) *reinterpret_cast<uint32_t*>(D.dst + o * P.c.token_stride) = div.codes(x);
+    }
+  }
+  if (lane == 0) *D.scale = now;
+  if (!__all_sync(kFull, fine) && lane == 0 && P.status != nullptr)
+    atomicOr(P.status, PKV_ST_NONFINITE);
+}
+
+// A run of any length that begins at token j0, read twice.
+template <typename T, bool INTER>
+__device__ __noinline__ void append_long(const AppendParams& P, const Target& D, int64_t n,
+                                         int64_t j0, int page, int lane) {
+  const int ps = P.c.page_size;
+  const int64_t slots = P.c.num_pages * ps;
+  const float before = *D.scale;
+  // The run's tokens from `base` on, 32 at a time: lane l holds base + l's
+  // slot (-1: not written) and position.  Returns how many are in the run.
   int slot = -1, pos = 0;
   auto scan = [&](int64_t base) -> int {
     const int64_t j = base + lane;
@@ -194,7 +279,7 @@ __device__ __forceinline__ void append_run(const AppendParams& P, int64_t n, int
       const bool inside = loc >= 0 && loc < slots;
       in_run = !inside || loc / ps == page;
       if (in_run && inside) {
-        pos = P.positions[j];
+        if (P.rot > 0) pos = P.positions[j];
         if (P.rot == 0 || (pos >= 0 && pos < P.max_pos)) slot = loc - page * ps;
       }
     }
@@ -203,143 +288,115 @@ __device__ __forceinline__ void append_run(const AppendParams& P, int64_t n, int
     if (lane >= cnt) slot = -1;
     return cnt;
   };
-  auto load = [&](int64_t base, int t) -> float4 {
+  auto load = [&](int64_t j, int t) -> float4 {
     uint2 raw = make_uint2(0u, 0u);
-    if (live) raw = *reinterpret_cast<const uint2*>(src + (base + t) * ts + lane * 4);
+    if (D.live) raw = *reinterpret_cast<const uint2*>(D.src + j * D.ts);
     float4 x = unpack4<T>(raw);
-    if (turning) {
+    if (D.turning) {
       const Turn turn = load_turn<INTER>(P, __shfl_sync(kFull, pos, t), lane);
       x = rotate<INTER>(P, x, turn, lane);
     }
     return x;
   };
-
-  int cnt = scan(j0);
-  const unsigned valid0 = __ballot_sync(kFull, slot >= 0);
   float amax = 0.0f;
   bool fine = true;
   int first = -1;  // the first written slot of the run
-  float4 held[kHold];
-  const bool hold = cnt <= kHold;
-  if (hold) {
-    if (valid0 == 0u) return;
-    first = __shfl_sync(kFull, slot, __ffs(valid0) - 1);
-#pragma unroll
-    for (int t = 0; t < kHold; ++t) {
-      if ((valid0 >> t) & 1u) {
-        held[t] = load(j0, t);
-        amax = fmaxf(amax, max4(held[t]));
-        fine = fine && finite4(held[t]);
+  for (int64_t base = j0;; base += 32) {
+    const int cnt = scan(base);
+    const unsigned valid = __ballot_sync(kFull, slot >= 0);
+    if (first < 0 && valid != 0u) first = __shfl_sync(kFull, slot, __ffs(valid) - 1);
+#pragma unroll 8
+    for (int t = 0; t < cnt; ++t) {
+      if ((valid >> t) & 1u) {
+        const float4 x = load(base + t, t);
+        amax = fmaxf(amax, max4(x));
+        fine = fine && finite4(x);
       }
     }
-  } else {
-    for (int64_t base = j0;;) {
-      const unsigned valid = __ballot_sync(kFull, slot >= 0);
-      if (first < 0 && valid != 0u) first = __shfl_sync(kFull, slot, __ffs(valid) - 1);
-#pragma unroll 4
-      for (int t = 0; t < cnt; ++t) {
-        if ((valid >> t) & 1u) {
-          const float4 x = load(base, t);
-          amax = fmaxf(amax, max4(x));
-          fine = fine && finite4(x);
-        }
-      }
-      if (cnt < 32) break;
-      base += 32;
-      cnt = scan(base);
-    }
-    if (first < 0) return;
+    if (cnt < 32) break;
   }
+  if (first < 0) return;
   amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
   const float want = scale_for(amax);
   const float now = first == 0 ? want : fmaxf(before, want);
-  // The page's earlier codes, when its scale grew.
-  if (first > 0 && now != before) {
-    const float ratio = before / now;
-    for (int t = 0; t < first; ++t) {
-      if (live) {
-        uint32_t* at = reinterpret_cast<uint32_t*>(dst + t * C.token_stride);
-        const uint32_t old = *at;
-        const uint32_t a = e4m3x2_to_f16x2(old), b = e4m3x2_to_f16x2(old >> 16);
-        const float2 x = Pair<__half>::unpack(a), y = Pair<__half>::unpack(b);
-        *at = e4m3x2(x.x * ratio, x.y * ratio) | (e4m3x2(y.x * ratio, y.y * ratio) << 16);
-      }
-    }
-  }
+  if (first > 0 && now != before) regrow(D.dst, P.c.token_stride, first, before, now, D.live);
   const Divide div(now);
-  if (hold) {
-#pragma unroll
-    for (int t = 0; t < kHold; ++t) {
-      if ((valid0 >> t) & 1u) {
+  for (int64_t base = j0;; base += 32) {
+    const int cnt = scan(base);
+    const unsigned valid = __ballot_sync(kFull, slot >= 0);
+#pragma unroll 8
+    for (int t = 0; t < cnt; ++t) {
+      if ((valid >> t) & 1u) {
+        const float4 x = load(base + t, t);
         const int o = __shfl_sync(kFull, slot, t);
-        if (live) *reinterpret_cast<uint32_t*>(dst + o * C.token_stride) = div.codes(held[t]);
+        if (D.live) *reinterpret_cast<uint32_t*>(D.dst + o * P.c.token_stride) = div.codes(x);
       }
     }
-  } else {
-    for (int64_t base = j0;;) {
-      cnt = scan(base);
-      const unsigned valid = __ballot_sync(kFull, slot >= 0);
-#pragma unroll 4
-      for (int t = 0; t < cnt; ++t) {
-        if ((valid >> t) & 1u) {
-          const float4 x = load(base, t);
-          const int o = __shfl_sync(kFull, slot, t);
-          if (live) *reinterpret_cast<uint32_t*>(dst + o * C.token_stride) = div.codes(x);
-        }
-      }
-      if (cnt < 32) break;
-      base += 32;
-    }
+    if (cnt < 32) break;
   }
-  if (lane == 0) *scale = now;
+  if (lane == 0) *D.scale = now;
   if (!__all_sync(kFull, fine) && lane == 0 && P.status != nullptr)
     atomicOr(P.status, PKV_ST_NONFINITE);
 }
 
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(const AppendParams P) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t n = P.n_tokens;
   if (P.total != nullptr) n = max(int64_t{0}, min(n, *P.total));
   const int ps = P.c.page_size;
   const int64_t slots = P.c.num_pages * ps;
   if (blockIdx.x < P.kv_blocks) {
-    // ---- this block's window of tokens: the runs that begin in it
+    // ---- this block's window of tokens: the runs that begin in it.  Lane l
+    // looks at token w0 + l; a run of at most kHold tokens ends within them.
     const int64_t w0 = static_cast<int64_t>(blockIdx.x) * P.window;
     const int64_t j = w0 + lane;
-    bool lead = false;
-    int page = -1, bad = 0;
-    if (lane < P.window && j < n) {
-      const int loc = P.out_loc[j];
-      if (loc >= 0 && loc < slots) {
-        page = loc / ps;
-        lead = true;
-        for (int64_t p = j - 1; p >= 0; --p) {  // past skipped tokens, if any
-          const int prev = P.out_loc[p];
-          if (prev < 0 || prev >= slots) continue;
+    int loc = -1, pos = 0, prev = -1;
+    if (j < n) {
+      loc = P.out_loc[j];
+      if (P.rot > 0) pos = P.positions[j];
+    }
+    if (lane == 0 && w0 > 0 && w0 <= n) prev = P.out_loc[w0 - 1];
+    const bool inside = loc >= 0 && loc < slots;
+    const int page = inside ? loc / ps : -1;
+    const bool placed = P.rot == 0 || (pos >= 0 && pos < P.max_pos);
+    const int before = __shfl_up_sync(kFull, loc, 1);
+    if (lane > 0) prev = before;
+    bool lead = lane < P.window && inside;
+    if (lead && j > 0) {
+      for (int64_t p = j - 1;;) {  // past skipped tokens, if any
+        if (prev >= 0 && prev < slots) {
           lead = prev / ps != page;
           break;
         }
-        if (P.rot > 0) {
-          const int pos = P.positions[j];
-          if (pos < 0 || pos >= P.max_pos) bad = PKV_ST_COL_OOB;
-        }
-      } else {
-        bad = PKV_ST_ROW_OOB;
+        if (--p < 0) break;
+        prev = P.out_loc[p];
       }
     }
-    if (warp == 0 && bad != 0 && P.status != nullptr) atomicOr(P.status, bad);
+    if (warp == 0 && lane < P.window && j < n && P.status != nullptr) {
+      const int bad = !inside ? PKV_ST_ROW_OOB : !placed ? PKV_ST_COL_OOB : 0;
+      if (bad != 0) atomicOr(P.status, bad);
+    }
     const unsigned leads = __ballot_sync(kFull, lead);
     const int per = 2 * P.c.kv_heads;
     const int items = __popc(leads) * per;
     for (int it = warp; it < items; it += kWarps) {
       unsigned m = leads;
       for (int r = it / per; r > 0; --r) m &= m - 1;
-      const int l = __ffs(m) - 1;
+      const int at = __ffs(m) - 1;
+      const int run_page = __shfl_sync(kFull, page, at);
+      const unsigned in_run = __ballot_sync(kFull, j < n && (!inside || page == run_page));
+      const unsigned valid = __ballot_sync(kFull, inside && page == run_page && placed) >> at;
+      const int cnt = __ffs(~(in_run >> at)) - 1;  // at <= 15: bit 31 - at and up are clear or past
       const int rest = it % per;
       const bool is_v = rest >= P.c.kv_heads;
-      append_run<T, INTER>(P, n, w0 + l, __shfl_sync(kFull, page, l),
-                           is_v ? rest - P.c.kv_heads : rest, is_v, lane);
+      const Target D = target(P, run_page, is_v ? rest - P.c.kv_heads : rest, is_v, lane);
+      if (cnt >= 0 && cnt <= kHold) {
+        append_held<T, INTER>(P, D, w0 + at, at, valid & ((1u << cnt) - 1u), loc - run_page * ps,
+                              pos, lane);
+      } else {
+        append_long<T, INTER>(P, D, n, w0 + at, run_page, lane);
+      }
     }
     return;
   }
@@ -350,13 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
   const int h0 = static_cast<int>(unit - j * groups) * kQHeads;
   if (j >= n) return;
   const int loc = P.out_loc[j];
-  if (loc < 0 || loc >= slots) return;
-  Turn turn;
-  if (P.rot > 0) {
-    const int pos = P.positions[j];
-    if (pos < 0 || pos >= P.max_pos) return;
-    turn = load_turn<INTER>(P, pos, lane);
-  }
+  const int pos = P.rot > 0 ? P.positions[j] : 0;
   const bool live = lane * 4 < P.c.head_dim;
   uint2 raw[kQHeads];
 #pragma unroll
@@ -364,6 +415,12 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
     raw[i] = make_uint2(0u, 0u);
     if (live && h0 + i < P.q_heads)
       raw[i] = *reinterpret_cast<const uint2*>(P.q + j * P.q_ts + (h0 + i) * P.q_hs + lane * 4);
+  }
+  if (loc < 0 || loc >= slots) return;
+  Turn turn;
+  if (P.rot > 0) {
+    if (pos < 0 || pos >= P.max_pos) return;
+    turn = load_turn<INTER>(P, pos, lane);
   }
 #pragma unroll
   for (int i = 0; i < kQHeads; ++i) {
