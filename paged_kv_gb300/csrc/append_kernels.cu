@@ -7,20 +7,22 @@
 // A run is the call's tokens of one page; its first token leads it.  One warp
 // owns one (run, head, k or v): it alone reads and writes that page's scale
 // and codes of that head, so nothing is shared between warps and a run's
-// result does not depend on the launch.  A head's row is spread over the lanes
-// in quads (4 elements, 8 bytes in, 4 bytes out); the rotate-half partner of
-// a quad lies a fixed number of lanes away and comes by one shuffle.  A run of
-// up to kHold tokens is loaded at once and stays in registers, unrotated,
-// between the maximum and the rounding: turning it twice costs less than the
-// registers of turned values, which would halve the warps that keep loads in
-// flight.  A longer run is read a second time, from L2.
+// result does not depend on the launch.
 //
-// Bound: bytes, and with few tokens the two dependent loads (a token's place,
-// then what the place needs).
+// A row (one token of one head) takes LPR lanes, each with two quads of 4
+// elements whose rotation stays inside the lane: with rotate-half, quad i and
+// the quad half the rotated width further on; a warp has 32 / LPR rows in
+// hand.  A run of up to kHold tokens is loaded at once and stays in registers,
+// unrotated, between the maximum and the rounding: turning it twice costs
+// fewer cycles than the registers of turned values, which would halve the
+// warps that keep loads in flight.  A longer run is read twice, from L2.
 //
 // e4m3 keeps its relative precision over 2^-6 .. 448, so a power-of-two scale
 // costs nothing against a tight one and lets a page's scale grow later
 // without a second rounding error (but for subnormals).
+//
+// Bound: bytes, and with few tokens the two dependent loads (a token's place,
+// then what the place needs).
 
 #include <cuda_runtime.h>
 
@@ -60,72 +62,74 @@ struct AppendParams {
   int rot, q_heads, window;
 };
 
-// The angle's cosines and sines for this lane's quad.
-struct Turn {
-  float c[4], s[4];
+// Which quads of a row a lane holds, and the angles they turn by.
+struct Lane {
+  int sub;        // row of the warp's 32 / LPR
+  int a, b;       // first elements of its two quads
+  int angle;      // cosines of cos_sin[p, angle ..]; < 0: not rotated
+  bool live;
 };
 
-template <bool INTER>
-__device__ __forceinline__ Turn load_turn(const AppendParams& P, int64_t pos, int lane) {
+template <int LPR, bool INTER>
+__device__ __forceinline__ Lane lane_of(const AppendParams& P, int lane) {
+  Lane L;
+  L.sub = lane / LPR;
+  const int l = lane % LPR, pairs = P.rot >> 3;
+  L.live = l * 8 < P.c.head_dim;
+  const bool turned = l < pairs;
+  L.a = turned && !INTER ? l * 4 : l * 8;
+  L.b = turned && !INTER ? l * 4 + (P.rot >> 1) : l * 8 + 4;
+  L.angle = turned ? l * 4 : -1;
+  return L;
+}
+
+struct Octet {
+  float a[4], b[4];
+};
+
+template <typename T>
+__device__ __forceinline__ Octet unpack8(uint2 x, uint2 y) {
+  const float2 p = Pair<T>::unpack(x.x), q = Pair<T>::unpack(x.y);
+  const float2 r = Pair<T>::unpack(y.x), s = Pair<T>::unpack(y.y);
+  return {{p.x, p.y, q.x, q.y}, {r.x, r.y, s.x, s.y}};
+}
+
+struct Turn {
+  float4 c, s;
+};
+
+__device__ __forceinline__ Turn load_turn(const AppendParams& P, const Lane& L, int pos) {
   Turn t;
-  const int half = P.rot >> 1;
-  const float* row = P.cos_sin + pos * P.rot;
-  if (INTER) {
-    if (lane * 4 < P.rot) {
-      const float2 c = *reinterpret_cast<const float2*>(row + 2 * lane);
-      const float2 s = *reinterpret_cast<const float2*>(row + half + 2 * lane);
-      t.c[0] = t.c[1] = c.x;
-      t.c[2] = t.c[3] = c.y;
-      t.s[0] = -s.x, t.s[1] = s.x, t.s[2] = -s.y, t.s[3] = s.y;
-      return t;
-    }
-  } else if (lane * 4 < P.rot) {
-    const bool second = lane * 4 >= half;
-    const int i = lane * 4 - (second ? half : 0);
-    const float4 c = *reinterpret_cast<const float4*>(row + i);
-    const float4 s = *reinterpret_cast<const float4*>(row + half + i);
-    t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
-    t.s[0] = second ? s.x : -s.x;
-    t.s[1] = second ? s.y : -s.y;
-    t.s[2] = second ? s.z : -s.z;
-    t.s[3] = second ? s.w : -s.w;
-    return t;
+  t.c = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+  t.s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (L.angle >= 0) {
+    const float* row = P.cos_sin + static_cast<int64_t>(pos) * P.rot + L.angle;
+    t.c = *reinterpret_cast<const float4*>(row);
+    t.s = *reinterpret_cast<const float4*>(row + (P.rot >> 1));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) t.c[i] = 1.0f, t.s[i] = 0.0f;
   return t;
 }
 
-// Rotates this lane's quad; every lane of the warp takes part.
-template <bool INTER>
-__device__ __forceinline__ float4 rotate(const AppendParams& P, float4 x, const Turn& t, int lane) {
-  float4 y;
-  if (INTER) {
-    y = make_float4(x.y, x.x, x.w, x.z);
-  } else {
-    const int quads = P.rot >> 3;  // quads in each half
-    int from = lane;
-    if (lane < quads) from = lane + quads;
-    else if (lane < 2 * quads) from = lane - quads;
-    y.x = __shfl_sync(kFull, x.x, from);
-    y.y = __shfl_sync(kFull, x.y, from);
-    y.z = __shfl_sync(kFull, x.z, from);
-    y.w = __shfl_sync(kFull, x.w, from);
-  }
-  // Elements past rot_dim have t.s = 0 and must not pick up 0 * inf.
-  if (lane * 4 < P.rot) {
-    x.x = fmaf(x.x, t.c[0], y.x * t.s[0]);
-    x.y = fmaf(x.y, t.c[1], y.y * t.s[1]);
-    x.z = fmaf(x.z, t.c[2], y.z * t.s[2]);
-    x.w = fmaf(x.w, t.c[3], y.w * t.s[3]);
-  }
-  return x;
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+  const float x = a, y = b;
+  a = fmaf(x, c, -(y * s));
+  b = fmaf(y, c, x * s);
 }
 
-template <typename T>
-__device__ __forceinline__ float4 unpack4(uint2 raw) {
-  const float2 a = Pair<T>::unpack(raw.x), b = Pair<T>::unpack(raw.y);
-  return make_float4(a.x, a.y, b.x, b.y);
+template <bool INTER>
+__device__ __forceinline__ void rotate(Octet& x, const Turn& t, const Lane& L) {
+  if (L.angle < 0) return;  // 0 * inf must not get in
+  if (INTER) {
+    turn_pair(x.a[0], x.a[1], t.c.x, t.s.x);
+    turn_pair(x.a[2], x.a[3], t.c.y, t.s.y);
+    turn_pair(x.b[0], x.b[1], t.c.z, t.s.z);
+    turn_pair(x.b[2], x.b[3], t.c.w, t.s.w);
+  } else {
+    turn_pair(x.a[0], x.b[0], t.c.x, t.s.x);
+    turn_pair(x.a[1], x.b[1], t.c.y, t.s.y);
+    turn_pair(x.a[2], x.b[2], t.c.z, t.s.z);
+    turn_pair(x.a[3], x.b[3], t.c.w, t.s.w);
+  }
 }
 
 // Least 2^e with a <= 448 * 2^e.  448 = 1.75 * 2^8, so e is the exponent of a
@@ -137,46 +141,37 @@ __device__ __forceinline__ float scale_for(float a) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ float finite_mag(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.0f;  // NaN and infinities do not count
+// Running maximum of magnitudes; a NaN or an infinity stays visible in it.
+__device__ __forceinline__ float max_all(float m, const Octet& x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmax_nan(m, fmax_nan(fabsf(x.a[i]), fabsf(x.b[i])));
+  return m;
 }
-
-__device__ __forceinline__ float max4(float4 x) {
-  return fmaxf(fmaxf(finite_mag(x.x), finite_mag(x.y)), fmaxf(finite_mag(x.z), finite_mag(x.w)));
-}
-
-__device__ __forceinline__ bool finite4(float4 x) {
-  return isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w);
-}
-
-// A divisor that multiplies where it can: powers of two (every scale this
-// kernel makes) by their exact reciprocal, other scales by division.
-struct Divide {
-  float s, inv;
-  bool power;
-  __device__ explicit Divide(float scale) {
-    s = scale;
-    inv = 1.0f / scale;
-    power = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+// The same over finite values only.
+__device__ __forceinline__ float max_finite(float m, const Octet& x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (isfinite(x.a[i])) m = fmaxf(m, fabsf(x.a[i]));
+    if (isfinite(x.b[i])) m = fmaxf(m, fabsf(x.b[i]));
   }
-  __device__ __forceinline__ uint32_t codes(float4 x) const {
-    if (power) {
-      x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-    } else {
-      x.x /= s, x.y /= s, x.z /= s, x.w /= s;
-    }
-    return e4m3x2(x.x, x.y) | (e4m3x2(x.z, x.w) << 16);
-  }
-};
+  return m;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* row, const Lane& L, const Octet& x, float inv) {
+  if (!L.live) return;
+  *reinterpret_cast<uint32_t*>(row + L.a) =
+      e4m3x2(x.a[0] * inv, x.a[1] * inv) | (e4m3x2(x.a[2] * inv, x.a[3] * inv) << 16);
+  *reinterpret_cast<uint32_t*>(row + L.b) =
+      e4m3x2(x.b[0] * inv, x.b[1] * inv) | (e4m3x2(x.b[2] * inv, x.b[3] * inv) << 16);
+}
 
 // Rounds the page's codes before slot `first` from one scale to a larger one.
-__device__ __forceinline__ void regrow(uint8_t* dst, int64_t token_stride, int first, float before,
-                                       float now, bool live) {
+__device__ __forceinline__ void regrow(uint8_t* dst, int64_t token_stride, int head_dim, int first,
+                                       float before, float now, int lane) {
   const float ratio = before / now;
   for (int t = 0; t < first; ++t) {
-    if (live) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(dst + t * token_stride);
+    if (lane * 4 < head_dim) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(dst + t * token_stride + lane * 4);
       const uint32_t old = *at;
       const float2 x = Pair<__half>::unpack(e4m3x2_to_f16x2(old));
       const float2 y = Pair<__half>::unpack(e4m3x2_to_f16x2(old >> 16));
@@ -191,82 +186,105 @@ struct Target {
   int64_t ts;
   uint8_t* dst;
   float* scale;
-  bool turning, live;
 };
 
-__device__ __forceinline__ Target target(const AppendParams& P, int page, int head, bool is_v,
-                                         int lane) {
+__device__ __forceinline__ Target target(const AppendParams& P, int page, int head, bool is_v) {
   const pkv_kv_cache& C = P.c;
   Target t;
-  t.src = (is_v ? P.v + head * P.v_hs : P.k + head * P.k_hs) + lane * 4;
+  t.src = is_v ? P.v + head * P.v_hs : P.k + head * P.k_hs;
   t.ts = is_v ? P.v_ts : P.k_ts;
-  t.dst = static_cast<uint8_t*>(is_v ? C.v : C.k) + page * C.page_stride + head * C.head_stride +
-          lane * 4;
+  t.dst = static_cast<uint8_t*>(is_v ? C.v : C.k) + page * C.page_stride + head * C.head_stride;
   t.scale = (is_v ? C.v_scale : C.k_scale) + static_cast<int64_t>(page) * C.kv_heads + head;
-  t.turning = !is_v && P.rot > 0;
-  t.live = lane * 4 < C.head_dim;
   return t;
 }
 
 // A run of at most kHold tokens.  Lane l holds token w0 + l's slot in the page
-// (-1: not written) and position; the run's tokens are j0 .. j0 + cnt - 1,
-// j0 = w0 + at.
-template <typename T, bool INTER>
-__device__ __forceinline__ void append_held(const AppendParams& P, const Target& D, int64_t j0,
-                                            int at, unsigned valid, int slot, int pos, int lane) {
+// and position; the run's tokens are j0 .. , j0 = w0 + at, those with a bit in
+// `valid` are written.
+template <typename T, int LPR, bool INTER, bool TURN>
+__device__ __forceinline__ void append_held(const AppendParams& P, const Target& D, const Lane& L,
+                                            int64_t j0, int at, unsigned valid, int slot, int pos,
+                                            int lane) {
+  constexpr int kRows = 32 / LPR, kIters = kHold / kRows;
   if (valid == 0u) return;
   const float before = *D.scale;
-  uint2 raw[kHold];
+  uint2 ra[kIters], rb[kIters];
+  const uint16_t* src = D.src + (j0 + L.sub) * D.ts;
 #pragma unroll
-  for (int t = 0; t < kHold; ++t) {
-    raw[t] = make_uint2(0u, 0u);
-    if (((valid >> t) & 1u) != 0u && D.live)
-      raw[t] = *reinterpret_cast<const uint2*>(D.src + (j0 + t) * D.ts);
+  for (int i = 0; i < kIters; ++i) {
+    ra[i] = rb[i] = make_uint2(0u, 0u);
+    if (((valid >> (i * kRows + L.sub)) & 1u) != 0u && L.live) {
+      ra[i] = *reinterpret_cast<const uint2*>(src + L.a);
+      rb[i] = *reinterpret_cast<const uint2*>(src + L.b);
+    }
+    src += kRows * D.ts;
   }
-  auto value = [&](int t) -> float4 {
-    float4 x = unpack4<T>(raw[t]);
-    if (D.turning) {
-      const Turn turn = load_turn<INTER>(P, __shfl_sync(kFull, pos, at + t), lane);
-      x = rotate<INTER>(P, x, turn, lane);
+  constexpr unsigned kGroup = (1u << kRows) - 1u;
+  auto value = [&](int i) -> Octet {
+    Octet x = unpack8<T>(ra[i], rb[i]);
+    if (TURN) {
+      const int t = i * kRows + L.sub;
+      const int p = __shfl_sync(kFull, pos, (at + t) & 31);
+      if ((valid >> t) & 1u) {
+        const Turn turn = load_turn(P, L, p);
+        rotate<INTER>(x, turn, L);
+      }
     }
     return x;
   };
   float amax = 0.0f;
-  bool fine = true;
 #pragma unroll
-  for (int t = 0; t < kHold; ++t) {
-    if ((valid >> t) & 1u) {
-      const float4 x = value(t);
-      amax = fmaxf(amax, max4(x));
-      fine = fine && finite4(x);
+  for (int i = 0; i < kIters; ++i) {
+    if ((valid >> (i * kRows)) & kGroup) amax = max_all(amax, value(i));
+  }
+  const bool fine = __all_sync(kFull, isfinite(amax));
+  if (!fine) {
+    amax = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < kIters; ++i) {
+      // (The registers are indexed by a loop that is not unrolled: rare.)
+      Octet x = {};
+#pragma unroll
+      for (int k = 0; k < kIters; ++k)
+        if (k == i) x = unpack8<T>(ra[k], rb[k]);
+      if (TURN) {
+        const int t = i * kRows + L.sub;
+        const int p = __shfl_sync(kFull, pos, (at + t) & 31);
+        if ((valid >> t) & 1u) rotate<INTER>(x, load_turn(P, L, p), L);
+      }
+      amax = max_finite(amax, x);
     }
   }
   amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
   const float want = scale_for(amax);
   const int first = __shfl_sync(kFull, slot, at + __ffs(valid) - 1);
   const float now = first == 0 ? want : fmaxf(before, want);
-  if (first > 0 && now != before) regrow(D.dst, P.c.token_stride, first, before, now, D.live);
-  const Divide div(now);
+  if (first > 0 && now != before)
+    regrow(D.dst, P.c.token_stride, P.c.head_dim, first, before, now, lane);
+  const float inv = 1.0f / now;
 #pragma unroll
-  for (int t = 0; t < kHold; ++t) {
-    if ((valid >> t) & 1u) {
-      const float4 x = value(t);
-      const int o = __shfl_sync(kFull, slot, at + t);
-      if (D.live) *reinterpret_cast<uint32_t*>(D.dst + o * P.c.token_stride) = div.codes(x);
+  for (int i = 0; i < kIters; ++i) {
+    if ((valid >> (i * kRows)) & kGroup) {
+      const int t = i * kRows + L.sub;
+      const Octet x = value(i);
+      const int o = __shfl_sync(kFull, slot, (at + t) & 31);
+      if ((valid >> t) & 1u) store_codes(D.dst + o * P.c.token_stride, L, x, inv);
     }
   }
   if (lane == 0) *D.scale = now;
-  if (!__all_sync(kFull, fine) && lane == 0 && P.status != nullptr)
-    atomicOr(P.status, PKV_ST_NONFINITE);
+  if (!fine && lane == 0 && P.status != nullptr) atomicOr(P.status, PKV_ST_NONFINITE);
 }
 
 // A run of any length that begins at token j0, read twice.
-template <typename T, bool INTER>
-__device__ __noinline__ void append_long(const AppendParams& P, const Target& D, int64_t n,
-                                         int64_t j0, int page, int lane) {
+template <typename T, int LPR, bool INTER>
+__device__ __noinline__ void append_long(const AppendParams& P, const Target D, int64_t n,
+                                         int64_t j0, int page, bool is_v, int lane) {
+  constexpr int kRows = 32 / LPR;
+  const Lane L = lane_of<LPR, INTER>(P, lane);
   const int ps = P.c.page_size;
   const int64_t slots = P.c.num_pages * ps;
   const float before = *D.scale;
+  const bool turning = !is_v && P.rot > 0;
   // The run's tokens from `base` on, 32 at a time: lane l holds base + l's
   // slot (-1: not written) and position.  Returns how many are in the run.
   int slot = -1, pos = 0;
@@ -288,64 +306,62 @@ __device__ __noinline__ void append_long(const AppendParams& P, const Target& D,
     if (lane >= cnt) slot = -1;
     return cnt;
   };
-  auto load = [&](int64_t j, int t) -> float4 {
-    uint2 raw = make_uint2(0u, 0u);
-    if (D.live) raw = *reinterpret_cast<const uint2*>(D.src + j * D.ts);
-    float4 x = unpack4<T>(raw);
-    if (D.turning) {
-      const Turn turn = load_turn<INTER>(P, __shfl_sync(kFull, pos, t), lane);
-      x = rotate<INTER>(P, x, turn, lane);
+  // Calls f(slot, values) for every row group of the run; slot < 0: not written.
+  auto each = [&](auto&& f) {
+    for (int64_t base = j0;; base += 32) {
+      const int cnt = scan(base);
+#pragma unroll 4
+      for (int t0 = 0; t0 < cnt; t0 += kRows) {
+        const int t = t0 + L.sub;
+        const int o = __shfl_sync(kFull, slot, t), p = __shfl_sync(kFull, pos, t);
+        uint2 a = make_uint2(0u, 0u), b = make_uint2(0u, 0u);
+        if (o >= 0 && L.live) {
+          const uint16_t* src = D.src + (base + t) * D.ts;
+          a = *reinterpret_cast<const uint2*>(src + L.a);
+          b = *reinterpret_cast<const uint2*>(src + L.b);
+        }
+        Octet x = unpack8<T>(a, b);
+        if (turning && o >= 0) rotate<INTER>(x, load_turn(P, L, p), L);
+        f(o, x);
+      }
+      if (cnt < 32) break;
     }
-    return x;
   };
   float amax = 0.0f;
-  bool fine = true;
-  int first = -1;  // the first written slot of the run
-  for (int64_t base = j0;; base += 32) {
-    const int cnt = scan(base);
-    const unsigned valid = __ballot_sync(kFull, slot >= 0);
-    if (first < 0 && valid != 0u) first = __shfl_sync(kFull, slot, __ffs(valid) - 1);
-#pragma unroll 8
-    for (int t = 0; t < cnt; ++t) {
-      if ((valid >> t) & 1u) {
-        const float4 x = load(base + t, t);
-        amax = fmaxf(amax, max4(x));
-        fine = fine && finite4(x);
-      }
-    }
-    if (cnt < 32) break;
+  int first = ps;  // the first written slot of the run
+  each([&](int o, const Octet& x) {
+    amax = max_all(amax, x);
+    if (o >= 0) first = min(first, o);
+  });
+  first = __reduce_min_sync(kFull, first);
+  if (first == ps) return;
+  const bool fine = __all_sync(kFull, isfinite(amax));
+  if (!fine) {
+    amax = 0.0f;
+    each([&](int, const Octet& x) { amax = max_finite(amax, x); });
   }
-  if (first < 0) return;
   amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
   const float want = scale_for(amax);
   const float now = first == 0 ? want : fmaxf(before, want);
-  if (first > 0 && now != before) regrow(D.dst, P.c.token_stride, first, before, now, D.live);
-  const Divide div(now);
-  for (int64_t base = j0;; base += 32) {
-    const int cnt = scan(base);
-    const unsigned valid = __ballot_sync(kFull, slot >= 0);
-#pragma unroll 8
-    for (int t = 0; t < cnt; ++t) {
-      if ((valid >> t) & 1u) {
-        const float4 x = load(base + t, t);
-        const int o = __shfl_sync(kFull, slot, t);
-        if (D.live) *reinterpret_cast<uint32_t*>(D.dst + o * P.c.token_stride) = div.codes(x);
-      }
-    }
-    if (cnt < 32) break;
-  }
+  if (first > 0 && now != before)
+    regrow(D.dst, P.c.token_stride, P.c.head_dim, first, before, now, lane);
+  const float inv = 1.0f / now;
+  each([&](int o, const Octet& x) {
+    if (o >= 0) store_codes(D.dst + o * P.c.token_stride, L, x, inv);
+  });
   if (lane == 0) *D.scale = now;
-  if (!__all_sync(kFull, fine) && lane == 0 && P.status != nullptr)
-    atomicOr(P.status, PKV_ST_NONFINITE);
+  if (!fine && lane == 0 && P.status != nullptr) atomicOr(P.status, PKV_ST_NONFINITE);
 }
 
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(const AppendParams P) {
+template <typename T, int LPR, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(
+    const __grid_constant__ AppendParams P) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t n = P.n_tokens;
   if (P.total != nullptr) n = max(int64_t{0}, min(n, *P.total));
   const int ps = P.c.page_size;
   const int64_t slots = P.c.num_pages * ps;
+  const Lane L = lane_of<LPR, INTER>(P, lane);
   if (blockIdx.x < P.kv_blocks) {
     // ---- this block's window of tokens: the runs that begin in it.  Lane l
     // looks at token w0 + l; a run of at most kHold tokens ends within them.
@@ -387,58 +403,77 @@ __global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(const AppendPara
       const int run_page = __shfl_sync(kFull, page, at);
       const unsigned in_run = __ballot_sync(kFull, j < n && (!inside || page == run_page));
       const unsigned valid = __ballot_sync(kFull, inside && page == run_page && placed) >> at;
-      const int cnt = __ffs(~(in_run >> at)) - 1;  // at <= 15: bit 31 - at and up are clear or past
+      const int cnt = __ffs(~(in_run >> at)) - 1;  // -1: all 32
       const int rest = it % per;
       const bool is_v = rest >= P.c.kv_heads;
-      const Target D = target(P, run_page, is_v ? rest - P.c.kv_heads : rest, is_v, lane);
-      if (cnt >= 0 && cnt <= kHold) {
-        append_held<T, INTER>(P, D, w0 + at, at, valid & ((1u << cnt) - 1u), loc - run_page * ps,
-                              pos, lane);
+      const Target D = target(P, run_page, is_v ? rest - P.c.kv_heads : rest, is_v);
+      if (cnt < 0 || cnt > kHold) {
+        append_long<T, LPR, INTER>(P, D, n, w0 + at, run_page, is_v, lane);
       } else {
-        append_long<T, INTER>(P, D, n, w0 + at, run_page, lane);
+        const unsigned mine = valid & ((1u << cnt) - 1u);
+        const int slot = loc - run_page * ps;
+        if (!is_v && P.rot > 0)
+          append_held<T, LPR, INTER, true>(P, D, L, w0 + at, at, mine, slot, pos, lane);
+        else
+          append_held<T, LPR, INTER, false>(P, D, L, w0 + at, at, mine, slot, pos, lane);
       }
     }
     return;
   }
   // ---- queries: kQHeads heads of one token a warp
+  constexpr int kRows = 32 / LPR, kIters = kQHeads / kRows;
   const int groups = (P.q_heads + kQHeads - 1) / kQHeads;
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) - P.kv_blocks) * kWarps + warp;
   const int64_t j = unit / groups;
-  const int h0 = static_cast<int>(unit - j * groups) * kQHeads;
+  const int h0 = static_cast<int>(unit - j * groups) * kQHeads + L.sub;
   if (j >= n) return;
   const int loc = P.out_loc[j];
   const int pos = P.rot > 0 ? P.positions[j] : 0;
-  const bool live = lane * 4 < P.c.head_dim;
-  uint2 raw[kQHeads];
+  uint2 ra[kIters], rb[kIters];
+  const uint16_t* src = P.q + j * P.q_ts + h0 * P.q_hs;
 #pragma unroll
-  for (int i = 0; i < kQHeads; ++i) {
-    raw[i] = make_uint2(0u, 0u);
-    if (live && h0 + i < P.q_heads)
-      raw[i] = *reinterpret_cast<const uint2*>(P.q + j * P.q_ts + (h0 + i) * P.q_hs + lane * 4);
+  for (int i = 0; i < kIters; ++i) {
+    ra[i] = rb[i] = make_uint2(0u, 0u);
+    if (L.live && h0 + i * kRows < P.q_heads) {
+      ra[i] = *reinterpret_cast<const uint2*>(src + L.a);
+      rb[i] = *reinterpret_cast<const uint2*>(src + L.b);
+    }
+    src += kRows * P.q_hs;
   }
   if (loc < 0 || loc >= slots) return;
   Turn turn;
   if (P.rot > 0) {
     if (pos < 0 || pos >= P.max_pos) return;
-    turn = load_turn<INTER>(P, pos, lane);
+    turn = load_turn(P, L, pos);
   }
+  uint16_t* dst = P.q_out + j * P.o_ts + h0 * P.o_hs;
 #pragma unroll
-  for (int i = 0; i < kQHeads; ++i) {
-    uint2 y = raw[i];
-    if (P.rot > 0) {
-      const float4 x = rotate<INTER>(P, unpack4<T>(raw[i]), turn, lane);
-      if (lane * 4 < P.rot) y = make_uint2(Pair<T>::pack(x.x, x.y), Pair<T>::pack(x.z, x.w));
+  for (int i = 0; i < kIters; ++i) {
+    uint2 ya = ra[i], yb = rb[i];
+    if (L.angle >= 0) {
+      Octet x = unpack8<T>(ra[i], rb[i]);
+      rotate<INTER>(x, turn, L);
+      ya = make_uint2(Pair<T>::pack(x.a[0], x.a[1]), Pair<T>::pack(x.a[2], x.a[3]));
+      yb = make_uint2(Pair<T>::pack(x.b[0], x.b[1]), Pair<T>::pack(x.b[2], x.b[3]));
     }
-    if (live && h0 + i < P.q_heads)
-      *reinterpret_cast<uint2*>(P.q_out + j * P.o_ts + (h0 + i) * P.o_hs + lane * 4) = y;
+    if (L.live && h0 + i * kRows < P.q_heads) {
+      *reinterpret_cast<uint2*>(dst + L.a) = ya;
+      *reinterpret_cast<uint2*>(dst + L.b) = yb;
+    }
+    dst += kRows * P.o_hs;
   }
 }
 
 template <typename T>
 void launch(const AppendParams& P, bool inter, int64_t blocks, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (inter) append_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(P);
-  else append_kernel<T, false><<<grid, kWarps * 32, 0, s>>>(P);
+  if (P.c.head_dim > 64) {
+    if (inter) append_kernel<T, 16, true><<<grid, kWarps * 32, 0, s>>>(P);
+    else append_kernel<T, 16, false><<<grid, kWarps * 32, 0, s>>>(P);
+  } else {
+    if (inter) append_kernel<T, 8, true><<<grid, kWarps * 32, 0, s>>>(P);
+    else append_kernel<T, 8, false><<<grid, kWarps * 32, 0, s>>>(P);
+  }
 }
 
 }  // namespace
