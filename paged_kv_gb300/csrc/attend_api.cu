@@ -12,6 +12,19 @@
 #include "kv_cache.cuh"
 #include "page_kernels.h"
 
+namespace {
+
+size_t workspace_need(int max_q_len, int group, int head_dim) {
+  const int sms = pkv::num_sms();
+  size_t partials =
+      pkv::row_partial_bytes(pkv::row_block(max_q_len, group), pkv::row_ctas(sms), head_dim);
+  if (pkv::has_tiles(max_q_len, group))
+    partials = std::max(partials, pkv::tile_partial_bytes(pkv::tile_ctas(sms), head_dim));
+  return pkv::counter_bytes(sms) + partials;
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_len, int q_heads,
@@ -20,8 +33,8 @@ size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_le
       kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || head_dim < 16 ||
       head_dim > PKV_MAX_HEAD_DIM)
     return 0;
-  const pkv::RowShape s = pkv::row_shape(max_q_len, q_heads / kv_heads, pkv::num_sms());
-  return pkv::row_workspace_bytes(s, head_dim);
+  max_q_len = static_cast<int>(std::min<int64_t>(max_q_len, std::max<int64_t>(n_tokens, 1)));
+  return workspace_need(max_q_len, q_heads / kv_heads, head_dim);
 }
 
 int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_token_stride,
@@ -58,8 +71,7 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
                 (long long)pt_rows, (long long)pt_cols);
   max_q_len = static_cast<int>(std::min<int64_t>(max_q_len, n_tokens));
   const int group = q_heads / cache->kv_heads;
-  const RowShape shape = row_shape(max_q_len, group, num_sms());
-  const size_t need = row_workspace_bytes(shape, cache->head_dim);
+  const size_t need = workspace_need(max_q_len, group, cache->head_dim);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(PKV_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (!aligned16(workspace)) return fail(PKV_EINVAL, "workspace is not 16-byte aligned");
@@ -85,11 +97,16 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   P.window = std::max(window, 0);
   P.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   P.bf16 = dt == PKV_BF16;
-  P.counters = static_cast<uint32_t*>(workspace);
-  P.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                        div_ceil(shape.max_ctas * 4, 256) * 256);
-  const cudaError_t e =
-      launch_attend_rows(P, shape, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = num_sms();
+  uint32_t* counters = static_cast<uint32_t*>(workspace);
+  P.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(sms));
+  P.counters = counters;
+  cudaError_t e = launch_attend_rows(P, row_block(max_q_len, group), row_ctas(sms), st);
+  if (e == cudaSuccess && has_tiles(max_q_len, group)) {
+    P.counters = counters + row_ctas(sms);
+    e = launch_attend_tiles(P, tile_ctas(sms), st);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();
 }

@@ -29,20 +29,36 @@ struct AttendParams {
   int window;                  // 0: none
   float scale_log2;            // sm_scale * log2(e)
   bool bf16;
-  // Workspace: one counter per CTA, then two partial results per CTA.
-  uint32_t* counters;
-  float* partials;
+  uint32_t* counters;          // the kernel's workspace: one counter per CTA,
+  float* partials;             // then two partial results per CTA
 };
 
-// Rows (query token, query head of one cache head) per block of the row
-// kernel, and its CTAs.
-struct RowShape {
-  int rows;      // 8 or 16
-  int max_ctas;
-};
-RowShape row_shape(int max_q_len, int group, int num_sms);
-// Workspace bytes of the row kernel.
-size_t row_workspace_bytes(const RowShape& s, int head_dim);
-cudaError_t launch_attend_rows(const AttendParams& P, const RowShape& s, cudaStream_t stream);
+// Requests of up to kRowLimit query rows a cache head go to the row kernel,
+// longer ones to the tile kernel.
+constexpr int kRowLimit = 32;
+inline bool has_tiles(int max_q_len, int group) {
+  return static_cast<int64_t>(max_q_len) * group > kRowLimit;
+}
+
+// The workspace begins with both kernels' counters, at places that depend on
+// the device alone, so that calls of any shape can follow one another on it.
+// The partial results come after; the kernels run one after the other and use
+// the same bytes for theirs.
+constexpr int kRowCtasPerSm = 2;
+inline int row_ctas(int num_sms) { return num_sms * kRowCtasPerSm; }
+inline int tile_ctas(int num_sms) { return num_sms; }
+inline size_t counter_bytes(int num_sms) {
+  return (static_cast<size_t>(row_ctas(num_sms) + 2 * tile_ctas(num_sms)) * 4 + 255) / 256 * 256;
+}
+
+// Rows (query token, query head of one cache head) in a block of the row
+// kernel: 8 or 16.
+int row_block(int max_q_len, int group);
+// Bytes of the kernels' partial results.
+size_t row_partial_bytes(int rows, int ctas, int head_dim);
+size_t tile_partial_bytes(int ctas, int head_dim);
+
+cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, cudaStream_t stream);
+cudaError_t launch_attend_tiles(const AttendParams& P, int ctas, cudaStream_t stream);
 
 }  // namespace pkv

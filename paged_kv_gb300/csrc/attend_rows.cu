@@ -32,6 +32,7 @@
 
 #include "api_common.h"
 #include "attend_params.h"
+#include "attend_units.cuh"
 #include "device_attr.h"
 #include "device_common.cuh"
 #include "kv_cache.cuh"
@@ -44,7 +45,6 @@ constexpr int kWarps = 4;
 constexpr int kStep = 16;                // positions a warp takes at a time
 constexpr int kTile = kWarps * kStep;    // positions of a work unit
 constexpr int kStages = 4;               // ring slots of a warp
-constexpr int kCtasPerSm = 2;
 constexpr float kLazy = 8.0f;            // log2 of how far sums may outgrow their reference
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -119,180 +119,23 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
 }
 
-// What the call asks of one request.
-struct Request {
-  int cached, table_row, begin;
-  int q_len;       // query tokens, at most n_tokens
-  int end;         // device_len where it can be read, 0 otherwise
-  int bad;
-};
-
-__device__ __forceinline__ Request load_request(const AttendParams& P, int i) {
-  Request r;
-  const int c = P.cached_len[i], d = P.device_len[i];
-  r.table_row = P.table_idx[i];
-  r.begin = P.kv_begin != nullptr ? max(0, P.kv_begin[i]) : 0;
-  const int64_t n = static_cast<int64_t>(d) - c;
-  r.cached = c;
-  r.q_len = static_cast<int>(max(int64_t{0}, min(n, P.n_tokens)));
-  r.end = d;
-  r.bad = 0;
-  if (r.q_len > 0) {
-    if (n > min(int64_t{P.max_q_len}, P.n_tokens)) r.bad |= PKV_ST_TOKEN_CAP;
-    if (r.table_row < 0 || r.table_row >= P.pt_rows) r.bad |= PKV_ST_ROW_OOB;
-    if (c < 0 || d > P.pt_cols) r.bad |= PKV_ST_COL_OOB;
-    if (r.bad != 0) r.end = 0;
-  }
-  return r;
-}
-
-// One block of rows: rows [row0, row0 + rows) of one request and cache head,
-// and the positions [start, end) that any of them sees.
-struct Block {
-  int row0, rows, start, end, tiles;
-};
-
-__device__ __forceinline__ Block make_block(const AttendParams& P, const Request& r, int b, int per) {
-  Block k;
-  k.row0 = b * per;
-  k.rows = min(per, r.q_len * P.group - k.row0);
-  const int t0 = k.row0 / P.group, t1 = (k.row0 + k.rows - 1) / P.group;
-  int lo = r.begin;
-  if (P.window > 0) lo = max(lo, r.cached + t0 - P.window + 1);
-  k.start = lo;
-  k.end = r.end == 0 ? lo : r.cached + t1 + 1;
-  if (k.end < k.start) k.end = k.start;
-  k.tiles = max(1, (k.end - k.start + kTile - 1) / kTile);
-  return k;
-}
-
-__device__ __forceinline__ int block_count(const AttendParams& P, const Request& r, int per) {
-  return static_cast<int>((static_cast<int64_t>(r.q_len) * P.group + per - 1) / per);
-}
-
-__device__ int64_t request_units(const AttendParams& P, const Request& r, int per) {
-  const int nb = block_count(P, r, per);
-  int64_t tiles = 0;
-  for (int b = 0; b < nb; ++b) tiles += make_block(P, r, b, per).tiles;
-  return tiles * P.c.kv_heads;
-}
-
-// A place in the call's units: what a warp loads from or computes on.
-struct Cursor {
-  Request r;
-  Block k;
-  int64_t q_off;   // the request's first packed token
-  int64_t left;    // units left in this CTA's range
-  int req, head, block, tile;
-};
-
-__device__ __forceinline__ void next_block(const AttendParams& P, Cursor& u, int per) {
-  u.tile = 0;
-  if (++u.block >= block_count(P, u.r, per)) {
-    u.block = 0;
-    if (++u.head >= P.c.kv_heads) {
-      u.head = 0;
-      do {
-        u.q_off += u.r.q_len;
-        ++u.req;
-        if (u.req >= P.B) return;
-        u.r = load_request(P, u.req);
-      } while (u.r.q_len == 0);
-    }
-  }
-  u.k = make_block(P, u.r, u.block, per);
-}
-
 template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attend_rows_kernel(const AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel(const AttendParams P) {
   using L = Layout<DP>;
   constexpr int kRows = 8 * NT;
   constexpr int kChunks = DP / 16;
+  constexpr UnitShape kShape{kRows, kTile, 1, kRowLimit};
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_o = reinterpret_cast<float*>(smem + L::kRing);
   float2* s_ml = reinterpret_cast<float2*>(s_o + kWarps * kRows * L::kPitch);
-  int64_t* s_head = reinterpret_cast<int64_t*>(s_ml + kWarps * kRows);  // 8 words
+  int* s_last = reinterpret_cast<int*>(s_ml + kWarps * kRows);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row_lane = lane >> 2, col_lane = lane & 3;
 
-  // ---- the call's units and where this CTA's range begins
-  {
-    const int per = (P.B + kWarps * 32 - 1) / (kWarps * 32);
-    const int i0 = min(P.B, tid * per), i1 = min(P.B, i0 + per);
-    long long units = 0, toks = 0;
-    int bad = 0;
-    for (int i = i0; i < i1; ++i) {
-      const Request r = load_request(P, i);
-      bad |= r.bad;
-      units += request_units(P, r, kRows);
-      toks += r.q_len;
-    }
-    long long ui = units, ti = toks;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(kFull, ui, o), b = __shfl_up_sync(kFull, ti, o);
-      if (lane >= o) ui += a, ti += b;
-    }
-    long long* s_w = reinterpret_cast<long long*>(smem);
-    if (lane == 31) s_w[warp] = ui, s_w[kWarps + warp] = ti;
-    __syncthreads();
-    long long ubase = ui - units, tbase = ti - toks, total = 0, ntok = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) ubase += s_w[w], tbase += s_w[kWarps + w];
-      total += s_w[w], ntok += s_w[kWarps + w];
-    }
-    if (blockIdx.x == 0 && P.status != nullptr) {
-      if (tid == 0 && ntok > P.n_tokens) bad |= PKV_ST_TOKEN_CAP;
-      if (bad != 0) atomicOr(P.status, bad);
-    }
-    const long long ctas = min(static_cast<long long>(gridDim.x), total);
-    const long long first = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-    if (first < total && ubase <= first && first < ubase + units) {
-      for (int i = i0; i < i1; ++i) {
-        const Request r = load_request(P, i);
-        const long long n = request_units(P, r, kRows);
-        if (first < ubase + n) {
-          s_head[0] = i;
-          s_head[1] = first - ubase;
-          s_head[2] = tbase;
-          break;
-        }
-        ubase += n;
-        tbase += r.q_len;
-      }
-    }
-    if (tid == 0) {
-      s_head[3] = total;
-      s_head[4] = ctas;
-    }
-    __syncthreads();
-  }
-  const int64_t total = s_head[3], ctas = s_head[4];
-  if (blockIdx.x >= ctas) return;
-  const int64_t first = blockIdx.x * total / ctas, last = (blockIdx.x + 1) * total / ctas;
-
   Cursor ld;  // where this warp loads
-  ld.req = static_cast<int>(s_head[0]);
-  ld.q_off = s_head[2];
-  ld.left = last - first;
-  ld.r = load_request(P, ld.req);
-  {
-    const int64_t per_head = request_units(P, ld.r, kRows) / P.c.kv_heads;
-    int64_t at = s_head[1];
-    ld.head = static_cast<int>(at / per_head);
-    at -= ld.head * per_head;
-    ld.block = 0;
-    for (;;) {
-      ld.k = make_block(P, ld.r, ld.block, kRows);
-      if (at < ld.k.tiles) break;
-      at -= ld.k.tiles;
-      ++ld.block;
-    }
-    ld.tile = static_cast<int>(at);
-  }
+  const Range range = find_range<kWarps * 32>(P, kShape, smem, &ld);
+  if (ld.left == 0) return;
   Cursor cu = ld;  // where it computes
-  __syncthreads();  // the scan's words in the ring are done with
 
   // Ring: columns past head_dim stay zero throughout.
   const uint32_t ring = smem_addr(smem) + warp * kStages * (L::kSlot + L::kScales);
@@ -349,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attend_rows_kernel(co
                         sc + static_cast<int64_t>(page) * P.c.kv_heads + ld.head, valid);
       }
       --ld.left;
-      if (++ld.tile >= ld.k.tiles && ld.left > 0) next_block(P, ld, kRows);
+      if (++ld.tile >= ld.k.tiles && ld.left > 0) next_block(P, ld, kShape);
       if (some) break;
     }
     cp_async_commit();
@@ -634,11 +477,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attend_rows_kernel(co
     };
     // Partial slots: 0 for a block that began in an earlier CTA, 1 for one
     // that begins here and goes on.
-    const int64_t seg_first = last - cu.left;              // this segment's first unit
+    const int64_t seg_first = range.last - cu.left;              // this segment's first unit
     const int64_t block_first = seg_first - t_begin;       // the block's first unit
-    const int64_t block_last = block_first + cu.k.tiles - 1;
-    const int64_t c0 = ((block_first + 1) * ctas - 1) / total;
-    const int64_t c1 = ((block_last + 1) * ctas - 1) / total;
+    int64_t c0, c1;
+    block_ctas(range, block_first, cu.k.tiles, &c0, &c1);
     const int quads = P.c.head_dim >> 2;
     const int pf_floats = partial_floats(kRows, DP);
     float* mine = P.partials + (2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * static_cast<int64_t>(pf_floats);
@@ -666,10 +508,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attend_rows_kernel(co
         const bool mine_last = before == static_cast<uint32_t>(c1 - c0);
         if (mine_last) P.counters[c0] = 0u;  // ready for the next call
         __threadfence();
-        s_head[5] = mine_last ? 1 : 0;
+        *s_last = mine_last ? 1 : 0;
       }
       __syncthreads();
-      if (s_head[5] != 0) {
+      if (*s_last != 0) {
         for (int i = tid; i < cu.k.rows * quads; i += kWarps * 32) {
           const int row = i / quads, d = (i - row * quads) * 4;
           Sum a{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
@@ -684,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attend_rows_kernel(co
     }
     __syncthreads();  // the joining buffer is free again
     cu.left -= t_end - t_begin;
-    if (cu.left > 0) next_block(P, cu, kRows);
+    if (cu.left > 0) next_block(P, cu, kShape);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -701,30 +543,26 @@ cudaError_t launch(const AttendParams& P, int ctas, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t launch_type(const AttendParams& P, const RowShape& s, cudaStream_t stream) {
+cudaError_t launch_type(const AttendParams& P, int rows, int ctas, cudaStream_t stream) {
   const bool wide = P.c.head_dim > 64;
-  if (s.rows == 8)
-    return wide ? launch<T, 128, 1>(P, s.max_ctas, stream) : launch<T, 64, 1>(P, s.max_ctas, stream);
-  return wide ? launch<T, 128, 2>(P, s.max_ctas, stream) : launch<T, 64, 2>(P, s.max_ctas, stream);
+  if (rows == 8)
+    return wide ? launch<T, 128, 1>(P, ctas, stream) : launch<T, 64, 1>(P, ctas, stream);
+  return wide ? launch<T, 128, 2>(P, ctas, stream) : launch<T, 64, 2>(P, ctas, stream);
 }
 
 }  // namespace
 
-RowShape row_shape(int max_q_len, int group, int num_sms) {
-  RowShape s;
-  s.rows = static_cast<int64_t>(max_q_len) * group <= 8 ? 8 : 16;
-  s.max_ctas = num_sms * kCtasPerSm;
-  return s;
+int row_block(int max_q_len, int group) {
+  return static_cast<int64_t>(max_q_len) * group <= 8 ? 8 : 16;
 }
 
-size_t row_workspace_bytes(const RowShape& s, int head_dim) {
-  const int dp = head_dim > 64 ? 128 : 64;
-  const size_t counters = (static_cast<size_t>(s.max_ctas) * 4 + 255) / 256 * 256;
-  return counters + static_cast<size_t>(s.max_ctas) * 2 * partial_floats(s.rows, dp) * 4;
+size_t row_partial_bytes(int rows, int ctas, int head_dim) {
+  return static_cast<size_t>(ctas) * 2 * partial_floats(rows, head_dim > 64 ? 128 : 64) * 4;
 }
 
-cudaError_t launch_attend_rows(const AttendParams& P, const RowShape& s, cudaStream_t stream) {
-  return P.bf16 ? launch_type<__nv_bfloat16>(P, s, stream) : launch_type<__half>(P, s, stream);
+cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, cudaStream_t stream) {
+  return P.bf16 ? launch_type<__nv_bfloat16>(P, rows, ctas, stream)
+                : launch_type<__half>(P, rows, ctas, stream);
 }
 
 }  // namespace pkv

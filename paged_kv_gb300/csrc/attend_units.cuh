@@ -1,0 +1,212 @@
+// How the attention kernels cut a call into work units.
+//
+// The query rows of one (request, cache head) -- row = query token * group +
+// query head in the group -- are cut into blocks of `rows`, the positions that
+// a block sees into tiles of `tile`.  A unit is one tile of one block; a call's
+// units are ordered by request, head, block, tile, and every CTA takes an
+// equal contiguous range of them.  A kernel takes only the requests whose row
+// count lies in [min_rows, max_rows]; others are another kernel's.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attend_params.h"
+#include "device_common.cuh"
+
+namespace pkv {
+
+struct UnitShape {
+  int rows, tile;
+  int64_t min_rows, max_rows;
+};
+
+// What the call asks of one request.
+struct Request {
+  int cached, table_row, begin;
+  int q_len;       // query tokens, at most n_tokens
+  int end;         // device_len where it can be read, 0 otherwise
+  int bad;
+};
+
+__device__ __forceinline__ Request load_request(const AttendParams& P, int i) {
+  Request r;
+  const int c = P.cached_len[i], d = P.device_len[i];
+  r.table_row = P.table_idx[i];
+  r.begin = P.kv_begin != nullptr ? max(0, P.kv_begin[i]) : 0;
+  const int64_t n = static_cast<int64_t>(d) - c;
+  r.cached = c;
+  r.q_len = static_cast<int>(max(int64_t{0}, min(n, P.n_tokens)));
+  r.end = d;
+  r.bad = 0;
+  if (r.q_len > 0) {
+    if (n > min(int64_t{P.max_q_len}, P.n_tokens)) r.bad |= PKV_ST_TOKEN_CAP;
+    if (r.table_row < 0 || r.table_row >= P.pt_rows) r.bad |= PKV_ST_ROW_OOB;
+    if (c < 0 || d > P.pt_cols) r.bad |= PKV_ST_COL_OOB;
+    if (r.bad != 0) r.end = 0;
+  }
+  return r;
+}
+
+// One block of rows: rows [row0, row0 + rows) of one request and cache head,
+// and the positions [start, end) that any of them sees.
+struct Block {
+  int row0, rows, start, end, tiles;
+};
+
+__device__ __forceinline__ Block make_block(const AttendParams& P, const Request& r, int b,
+                                            const UnitShape& u) {
+  Block k;
+  k.row0 = b * u.rows;
+  k.rows = min(u.rows, r.q_len * P.group - k.row0);
+  const int t0 = k.row0 / P.group, t1 = (k.row0 + k.rows - 1) / P.group;
+  int lo = r.begin;
+  if (P.window > 0) lo = max(lo, r.cached + t0 - P.window + 1);
+  k.start = lo;
+  k.end = r.end == 0 ? lo : r.cached + t1 + 1;
+  if (k.end < k.start) k.end = k.start;
+  k.tiles = max(1, (k.end - k.start + u.tile - 1) / u.tile);
+  return k;
+}
+
+// Blocks of one (request, cache head) that this kernel takes.
+__device__ __forceinline__ int block_count(const AttendParams& P, const Request& r,
+                                           const UnitShape& u) {
+  const int64_t n = static_cast<int64_t>(r.q_len) * P.group;
+  if (n < u.min_rows || n > u.max_rows) return 0;
+  return static_cast<int>((n + u.rows - 1) / u.rows);
+}
+
+__device__ __forceinline__ int64_t request_units(const AttendParams& P, const Request& r,
+                                                 const UnitShape& u) {
+  const int nb = block_count(P, r, u);
+  int64_t tiles = 0;
+  for (int b = 0; b < nb; ++b) tiles += make_block(P, r, b, u).tiles;
+  return tiles * P.c.kv_heads;
+}
+
+// A place in the call's units: what a warp loads from or computes on.
+struct Cursor {
+  Request r;
+  Block k;
+  int64_t q_off;   // the request's first packed token
+  int64_t left;    // units left in this CTA's range
+  int req, head, block, tile;
+};
+
+// Goes to the next block.  Only called while units are left.
+__device__ __forceinline__ void next_block(const AttendParams& P, Cursor& c, const UnitShape& u) {
+  c.tile = 0;
+  if (++c.block >= block_count(P, c.r, u)) {
+    c.block = 0;
+    if (++c.head >= P.c.kv_heads) {
+      c.head = 0;
+      do {
+        c.q_off += c.r.q_len;
+        ++c.req;
+        if (c.req >= P.B) return;
+        c.r = load_request(P, c.req);
+      } while (block_count(P, c.r, u) == 0);
+    }
+  }
+  c.k = make_block(P, c.r, c.block, u);
+}
+
+// A CTA's range of the call's units.
+struct Range {
+  int64_t total;   // the call's units
+  int64_t ctas;    // CTAs that have any
+  int64_t last;    // one past this CTA's last unit
+};
+
+// Finds this CTA's range and sets *c to its first unit (c->left 0: none).
+// All THREADS of the CTA take part; `scratch` is 512 bytes of shared memory,
+// free again on return.  Block 0 reports the requests' errors.
+template <int THREADS>
+__device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scratch, Cursor* c) {
+  constexpr int kW = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long* s_w = static_cast<long long*>(scratch);
+  long long* s_at = s_w + 2 * kW;
+  const int per = (P.B + THREADS - 1) / THREADS;
+  const int i0 = min(P.B, tid * per), i1 = min(P.B, i0 + per);
+  long long units = 0, toks = 0;
+  int bad = 0;
+  for (int i = i0; i < i1; ++i) {
+    const Request r = load_request(P, i);
+    bad |= r.bad;
+    units += request_units(P, r, u);
+    toks += r.q_len;
+  }
+  long long ui = units, ti = toks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(kFull, ui, o), b = __shfl_up_sync(kFull, ti, o);
+    if (lane >= o) ui += a, ti += b;
+  }
+  if (lane == 31) s_w[warp] = ui, s_w[kW + warp] = ti;
+  __syncthreads();
+  long long ubase = ui - units, tbase = ti - toks, total = 0, ntok = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) ubase += s_w[w], tbase += s_w[kW + w];
+    total += s_w[w], ntok += s_w[kW + w];
+  }
+  if (blockIdx.x == 0 && P.status != nullptr) {
+    if (tid == 0 && ntok > P.n_tokens) bad |= PKV_ST_TOKEN_CAP;
+    if (bad != 0) atomicOr(P.status, bad);
+  }
+  Range g;
+  g.total = total;
+  g.ctas = min(static_cast<long long>(gridDim.x), total);
+  if (blockIdx.x >= g.ctas) {
+    c->left = 0;
+    g.last = total;
+    return g;
+  }
+  const long long first = blockIdx.x * total / g.ctas;
+  g.last = (blockIdx.x + 1ll) * total / g.ctas;
+  if (ubase <= first && first < ubase + units) {
+    for (int i = i0; i < i1; ++i) {
+      const Request r = load_request(P, i);
+      const long long n = request_units(P, r, u);
+      if (first < ubase + n) {
+        s_at[0] = i;
+        s_at[1] = first - ubase;
+        s_at[2] = tbase;
+        break;
+      }
+      ubase += n;
+      tbase += r.q_len;
+    }
+  }
+  __syncthreads();
+  c->req = static_cast<int>(s_at[0]);
+  c->q_off = s_at[2];
+  c->left = g.last - first;
+  c->r = load_request(P, c->req);
+  long long at = s_at[1];
+  const long long per_head = request_units(P, c->r, u) / P.c.kv_heads;
+  c->head = static_cast<int>(at / per_head);
+  at -= c->head * per_head;
+  c->block = 0;
+  for (;;) {
+    c->k = make_block(P, c->r, c->block, u);
+    if (at < c->k.tiles) break;
+    at -= c->k.tiles;
+    ++c->block;
+  }
+  c->tile = static_cast<int>(at);
+  __syncthreads();
+  return g;
+}
+
+// The CTAs that hold a block's first and last unit, given its first unit.
+__device__ __forceinline__ void block_ctas(const Range& g, int64_t block_first, int tiles,
+                                           int64_t* c0, int64_t* c1) {
+  *c0 = ((block_first + 1) * g.ctas - 1) / g.total;
+  *c1 = ((block_first + tiles) * g.ctas - 1) / g.total;
+}
+
+}  // namespace pkv

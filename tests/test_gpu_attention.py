@@ -318,3 +318,22 @@ def test_two_streams_with_their_own_workspaces_and_a_graph(new):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.cpu().double(), want)
+
+
+def test_calls_of_different_shapes_share_a_workspace():
+    # Each leaves the workspace ready for the next, whatever its shape.
+    problems = []
+    for i, (cached, new, hkv, group, d) in enumerate([
+            ([9000], [1], 1, 16, 128), ([5000], [300], 1, 1, 64), ([4000, 9], [2, 5], 1, 4, 64),
+            ([3000], [200], 2, 1, 128), ([7000], [1], 1, 1, 64)]):
+        p = ref.page_problem(cached, new, 16, hkv, d, 60 + i)
+        q = queries(sum(new), hkv * group, d, torch.bfloat16, i)
+        problems.append((p, make_cache(p), q))
+    size = max(pkv.paged_attention_workspace_bytes(len(p["cached_len"]), q.shape[0], p["max_q_len"],
+                                                   q.shape[1], c.kv_heads, q.shape[2])
+               for p, c, q in problems)
+    fresh = [call(p, c, q, workspace=torch.zeros(size, dtype=torch.uint8))[0] for p, c, q in problems]
+    shared = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for (p, c, q), want in zip(problems, fresh):
+            assert torch.equal(call(p, c, q, workspace=shared)[0], want)
