@@ -77,6 +77,7 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   if (!aligned16(workspace)) return fail(PKV_EINVAL, "workspace is not 16-byte aligned");
   AttendParams P;
   P.c = *cache;
+  P.page_div = Divider::by(static_cast<uint32_t>(cache->page_size));
   P.q = static_cast<const uint16_t*>(q);
   P.out = static_cast<uint16_t*>(out);
   P.lse = lse;

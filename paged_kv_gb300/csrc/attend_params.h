@@ -10,8 +10,28 @@
 
 namespace pkv {
 
+// Division of 31-bit numbers by a constant: floor(x / d) = (x * mul) >> (31 + shift)
+// with shift = ceil(log2 d), mul = ceil(2^(31 + shift) / d) < 2^32.  (Write
+// mul d = 2^(31 + shift) + e with 0 <= e < d <= 2^shift: x e < 2^(31 + shift),
+// so x mul / 2^(31 + shift) exceeds x / d by less than 1 / d.)
+struct Divider {
+  uint32_t mul, shift;
+  static Divider by(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t{1} << s) < d) ++s;
+    return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s};
+  }
+#ifdef __CUDACC__
+  __device__
+#endif
+  uint32_t divide(uint32_t x) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(x) * mul) >> shift);
+  }
+};
+
 struct AttendParams {
   pkv_kv_cache c;
+  Divider page_div;            // by c.page_size
   const uint16_t* q;
   uint16_t* out;
   float* lse;                  // or nullptr

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         const uint32_t slot = ring + (issued % kStages) * (L::kSlot + L::kScales);
         ++issued;
         const int tok = base + (lane & 15);
-        bool valid = tok < ld.k.end;
+        bool valid = tok >= ld.k.lo && tok < ld.k.end;
         int loc = 0;
         if (valid) loc = P.page_table[ld.r.table_row * P.pt_cols + tok];
         if (loc < 0 || loc >= slots) {
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           loc = 0;
           valid = false;
         }
-        const int page = loc / ps;
+        const int page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(loc)));
         const int64_t at = page * P.c.page_stride + (loc - page * ps) * P.c.token_stride +
                            ld.head * P.c.head_stride;
         const unsigned ok = __ballot_sync(kFull, valid);

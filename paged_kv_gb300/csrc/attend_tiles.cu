@@ -8,20 +8,21 @@
 //     rows, exactly: 4 significant bits each, so 2 for bf16 and 3 for fp16
 //     (elements below 2^-9 of a row's largest keep an absolute 2^-17 of it);
 //   S times the page's key scale and the row's factor, softmax in fp32;
-//   O[128 x D] += P V      on kind::f16: P is bf16 in tensor memory, in S's
-//     place; V is made bf16 (code times page scale) on its way to shared
-//     memory.  bf16 on both sides because weights and scales need its range: a
-//     long context's weights may lie 2^-20 below an early large one and still
-//     add up to as much.
-// The running maximum m moves only when it would rise by more than 8 (in
-// log2): then O is rescaled in tensor memory by the row's own thread.
+//   O[128 x D] += P V      on kind::f16: V's codes made fp16 (exactly) on their
+//     way to shared memory, P = 2^7 2^(s - m) vs in fp16 in tensor memory, in
+//     S's place, with the page's value scale in it and m the running maximum
+//     of s + log2 vs.  m moves only when it would rise by more than 8, so P
+//     stays below 2^15 and keeps fp16's 11 bits down to 2^-22 of the largest:
+//     a long context's weights may lie far below an early large one and still
+//     add up to as much.  l sums 2^(s - m) in fp32.
+// When m moves, O is rescaled in tensor memory by the row's own thread.
 //
 // Roles (16 warps): warps 0-3 and 4-7 are the softmax of tile 0 and 1, a
-// thread a row; warps 8-11 load: K by cp.async, V through registers (converted
-// there), page places and scales a unit ahead; one thread of warp 12 issues
-// the products.  While one tile is in its softmax the other's products run.
+// thread a row; warps 8-11 bring V, converting it in registers; warp 12 issues
+// the products; warps 13-15 look up the positions' places and scales and bring
+// K by cp.async.  While one tile is in its softmax the other's products run.
 //   k_full/k_empty, v_full/v_empty: rings of units in shared memory;
-//   sc_full: the units' key scales;  q_full[t]: the block's queries;
+//   sc_full/sc_empty: places and scales;  q_full[t]: the block's queries;
 //   s_full[t]: S is there, and O and P of the unit before are done with;
 //   p_full[t]: P is there (and O rescaled), S may be overwritten.
 // Products of one thread run in issue order, so P V and the next Q K^T of a
@@ -53,6 +54,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kPlaceThreads = 96;
 constexpr int kTileRows = 128;
 constexpr int kBlockRows = 2 * kTileRows;
 constexpr int kTile = 128;               // positions of a unit
@@ -62,6 +64,7 @@ constexpr int kKBytes = kTile * kPitch;
 constexpr int kVHalf = kTile * 128;      // 64 channels of bf16
 constexpr int kVBytes = 2 * kVHalf;
 constexpr float kLazy = 8.0f;
+constexpr float kWeight = 128.0f;        // weights are this times 2^(s - m) vs
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr long long kWaitNs = 2000000000ll;
 __host__ __device__ constexpr UnitShape unit_shape() {
@@ -76,19 +79,20 @@ struct Plan {
   static constexpr int q = 0;
   static constexpr int k = q + 2 * NS * kQBytes;
   static constexpr int v = k + kK * kKBytes;
-  static constexpr int sc = v + kV * kVBytes;        // key scales, kSc slots
-  static constexpr int vs = sc + kSc * kTile * 4;    // value scales, 3 slots
-  static constexpr int off = vs + 3 * kTile * 4;     // byte offsets, 3 slots
-  static constexpr int bar = off + 3 * kTile * 8;
+  static constexpr int sc = v + kV * kVBytes;        // scales, kSc slots: ks, log2 vs, vs
+  static constexpr int off = sc + kSc * 3 * kTile * 4;  // byte offsets
+  static constexpr int bar = off + kSc * kTile * 8;
   static constexpr int bytes = bar + 512 + 1024;     // and room to align
 };
 
 struct Bars {
-  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], sc_full[4];
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], sc_full[4], sc_empty[4];
   uint64_t q_full[2], s_full[2], p_full[2];
   uint32_t tmem;
   int dead;
   int last[2];
+  int partial[4];
+  int mixed[4][3];   // a group of 16 positions spans pages
   int nan;
 };
 
@@ -101,21 +105,43 @@ struct Ring {
   }
 };
 
+// By whole warps, which leave it converged: what follows may be an instruction
+// that all lanes have to issue together.
 __device__ __forceinline__ void wait(Bars* B, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
-  const long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*reinterpret_cast<volatile int*>(&B->dead) != 0) return;
-    if (globaltimer_ns() - t0 > kWaitNs) {
-      *reinterpret_cast<volatile int*>(&B->dead) = 1;
-      return;
+  if (!mbar_try_wait(bar, parity)) {
+    const long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*reinterpret_cast<volatile int*>(&B->dead) != 0) break;
+      if (globaltimer_ns() - t0 > kWaitNs) {
+        *reinterpret_cast<volatile int*>(&B->dead) = 1;
+        break;
+      }
     }
   }
+  __syncwarp();
+}
+
+// One arrival a warp (32 arrivals on one word would take their turns).
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 template <int ID>
 __device__ __forceinline__ void bar_sync(int id_add = 0) {
+  __syncwarp();
   asm volatile("bar.sync %0, 128;" ::"r"(ID + id_add) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Two fp32 at a time.
@@ -157,232 +183,432 @@ __host__ __device__ constexpr int64_t partial_floats(int head_dim) {
 
 // ------------------------------------------------------------------ loading
 
+// Three warps: finds the places of a unit's positions in the cache, two units
+// ahead (unit J's table entries are read at J - 2, its scales at J - 1), and
+// copies K.  A thread has positions tid and tid + 96 (below 128).
 template <int NS>
-__device__ void load_role(const AttendParams& P, Cursor c, uint8_t* smem, Bars* B) {
+__device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t* smem, Bars* B) {
   using L = Plan<NS>;
-  const int tid = threadIdx.x & 127;
-  const int ps = P.c.page_size;
-  const int slots = static_cast<int>(P.c.num_pages * ps);
+  const int tid = threadIdx.x - 13 * 32;
+  const int units = static_cast<int>(a.left);
+  const int slots = static_cast<int>(P.c.num_pages * P.c.page_size);
   const int chunks = P.c.head_dim >> 4;
-  const int ch = tid & 7, t0 = tid >> 3;
-  const bool mine = ch < chunks;
   float* s_sc = reinterpret_cast<float*>(smem + L::sc);
-  float* s_vs = reinterpret_cast<float*>(smem + L::vs);
   int64_t* s_off = reinterpret_cast<int64_t*>(smem + L::off);
+  constexpr int kPer = 2;
+  const bool second = tid + kPlaceThreads < kTile;
 
-  // Places run two units ahead of the loads: unit u's table entry is read at
-  // u - 2, its scales at u - 1.
-  Cursor a = c;               // the unit whose table entry is read next
-  auto step = [&](Cursor& x) {
-    --x.left;
-    if (++x.tile >= x.k.tiles && x.left > 0) next_block(P, x, unit_shape());
+  // A place outside the block's positions takes the nearest one's location, for
+  // its scales alone; loc -1: outside the cache, or no position at all.
+  struct Places { int loc[kPer]; bool in[kPer]; int head; bool partial; };
+  int all_lo = 0, all_hi = 0;
+  auto block_bounds = [&]() {  // positions that every row of the block sees
+    const int t_first = a.k.row0 / P.group, t_last = (a.k.row0 + a.k.rows - 1) / P.group;
+    all_lo = a.r.begin;
+    if (P.window > 0) all_lo = max(all_lo, a.r.cached + t_last - P.window + 1);
+    all_hi = min(a.r.cached + t_first, a.k.end - 1);
   };
-  struct Place { int loc, head; };  // loc -1: nothing there
-  auto read_place = [&]() -> Place {
-    Place p{-1, 0};
+  block_bounds();
+  auto read_places = [&]() -> Places {
+    Places p;
+    p.loc[0] = p.loc[1] = -1;
+    p.in[0] = p.in[1] = false;
+    p.head = 0;
+    p.partial = false;
     if (a.left > 0) {
-      const int tok = a.k.start + a.tile * kTile + tid;
-      if (tok < a.k.end) {
-        p.loc = P.page_table[a.r.table_row * P.pt_cols + tok];
-        if (p.loc < 0 || p.loc >= slots) {
-          if (P.status != nullptr) atomicOr(P.status, PKV_ST_ROW_OOB);
-          p.loc = -1;
+      const int base = a.k.start + a.tile * kTile;
+      const int32_t* row = P.page_table + a.r.table_row * P.pt_cols;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int tok = base + tid + i * kPlaceThreads;
+        if (a.k.lo < a.k.end && (i == 0 || second)) {
+          const int near = max(a.k.lo, min(tok, a.k.end - 1));
+          p.in[i] = near == tok;
+          p.loc[i] = row[near];
+          if (p.loc[i] < 0 || p.loc[i] >= slots) {
+            if (P.status != nullptr) atomicOr(P.status, PKV_ST_ROW_OOB);
+            p.loc[i] = -1;
+          }
         }
       }
       p.head = a.head;
-      step(a);
+      p.partial = base < all_lo || base + kTile - 1 > all_hi;
+      --a.left;
+      if (++a.tile >= a.k.tiles && a.left > 0) {
+        next_block(P, a, unit_shape());
+        block_bounds();
+      }
     }
     return p;
   };
-  float ks = 0.0f, vs = 0.0f;
-  auto resolve = [&](const Place& p, int slot) {  // byte offsets, and the scales' loads
-    int64_t off = -1;
-    ks = vs = 0.0f;
-    if (p.loc >= 0) {
-      const int page = p.loc / ps;
-      off = page * P.c.page_stride + (p.loc - page * ps) * P.c.token_stride +
-            p.head * P.c.head_stride;
-      const int64_t s = static_cast<int64_t>(page) * P.c.kv_heads + p.head;
-      ks = P.c.k_scale[s];
-      vs = P.c.v_scale[s];
-    }
-    s_off[slot * kTile + tid] = off;
-  };
-
-  Ring kr, vr, sr;
-  int three = 0;              // slot of unit i's places
-  uint4 raw[8];
-  bool pending = false;       // V of the unit before is in `raw`
-  bool pending_partial = false;
-  int pending_three = 0;
-  auto convert = [&]() {
-    wait(B, &B->v_empty[vr.slot], vr.phase ^ 1u);
-    uint8_t* dst = smem + L::v + vr.slot * kVBytes + (ch >> 2) * kVHalf;
-    bool nan = false;
+  float ks[kPer], vs[kPer];
+  auto resolve = [&](const Places& p, int slot) {  // byte offsets, and the scales' loads
+    bool mixed = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = t0 + 16 * i;
-      const float scale = s_vs[pending_three * kTile + t];
-      uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      if (pending_partial) {
-        // A NaN that some row does not see: zero here, put back at the end.
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t hit = (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-          if (hit != 0u) nan = true;
-          w[k] &= ~(hit * 255u);
-        }
+    for (int i = 0; i < kPer; ++i) {
+      int64_t off = -1;
+      int page = -1;
+      ks[i] = 1.0f;  // (of a zero key; it must not turn a masked -inf into NaN)
+      vs[i] = 0.0f;
+      if (p.loc[i] >= 0) {
+        page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(p.loc[i])));
+        if (p.in[i])
+          off = page * P.c.page_stride + (p.loc[i] - page * P.c.page_size) * P.c.token_stride +
+                p.head * P.c.head_stride;
+        const int64_t s = static_cast<int64_t>(page) * P.c.kv_heads + p.head;
+        ks[i] = P.c.k_scale[s];
+        vs[i] = P.c.v_scale[s];
       }
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = Pair<__half>::unpack(e4m3x2_to_f16x2(w[k]));
-        const float2 y = Pair<__half>::unpack(e4m3x2_to_f16x2(w[k] >> 16));
-        o[2 * k] = Pair<__nv_bfloat16>::pack(x.x * scale, x.y * scale);
-        o[2 * k + 1] = Pair<__nv_bfloat16>::pack(y.x * scale, y.y * scale);
-      }
-      if (mine) {
-        // 32 bytes: chunks 2 (ch % 4) and the next; the halves' lanes store
-        // them in opposite order, so that a quarter warp covers all banks.
-        const int c0 = (ch & 3) * 2, swap = ch >> 2;
-        uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint4*>(dst + chunk_at(t, c0 + swap)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + chunk_at(t, c0 + 1 - swap)) = swap ? lo : hi;
+      if (i == 0 || second) {
+        s_off[slot * kTile + tid + i * kPlaceThreads] = off;
+        const int first = __shfl_sync(kFull, page, threadIdx.x & 16);  // whole warps
+        mixed |= page != first;
       }
     }
-    if (nan) *reinterpret_cast<volatile int*>(&B->nan) = 1;
-    tc::fence_smem();
-    mbar_arrive(&B->v_full[vr.slot]);
-    vr.next(L::kV);
+    mixed = __any_sync(kFull, mixed);
+    if ((tid & 31) == 0) B->mixed[slot][tid >> 5] = mixed ? 1 : 0;
+    if (tid == 0) B->partial[slot] = p.partial ? 1 : 0;
   };
-
-  Place ahead = read_place();
+  Ring kr, er;                 // K slots; the place slots being reused
+  er.slot = 1;
+  Places ahead = read_places();
   resolve(ahead, 0);
-  ahead = read_place();
-  while (c.left > 0) {
-    // ---- this unit's scales; the next one's offsets; the one after's entry
-    s_sc[sr.slot * kTile + tid] = ks;
-    s_vs[three * kTile + tid] = vs;
-    const int next_three = three == 2 ? 0 : three + 1;
-    resolve(ahead, next_three);
-    ahead = read_place();
-    bar_sync<1>();
-    mbar_arrive(&B->sc_full[sr.slot]);
-    sr.next(L::kSc);
-    // ---- K
-    wait(B, &B->k_empty[kr.slot], kr.phase ^ 1u);
-    const int64_t* offs = s_off + three * kTile + t0;
-    const uint32_t kdst = smem_addr(smem + L::k + kr.slot * kKBytes);
-    if (mine) {
+  ahead = read_places();
+  for (int u = 0; u < units; ++u) {
+    const int slot = u % L::kSc, next = (u + 1) % L::kSc;
+    float k0[kPer], v0[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t off = offs[16 * i];
-        const uint8_t* src = static_cast<const uint8_t*>(P.c.k) + (off < 0 ? 0 : off) + ch * 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     ::"r"(kdst + chunk_at(t0 + 16 * i, ch)), "l"(src), "r"(off < 0 ? 0 : 16)
-                     : "memory");
+    for (int i = 0; i < kPer; ++i) k0[i] = ks[i], v0[i] = vs[i];
+    if (u + 1 < units) {
+      wait(B, &B->sc_empty[er.slot], er.phase ^ 1u);  // the values' warps are done with it
+      er.next(L::kSc);
+      resolve(ahead, next);
+      ahead = read_places();
+    }
+    // A unit kSc earlier is through its softmax once K's slot is free again.
+    wait(B, &B->k_empty[kr.slot], kr.phase ^ 1u);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i == 0 || second) {
+        float* at = s_sc + slot * 3 * kTile + tid + i * kPlaceThreads;
+        at[0] = k0[i];
+        at[kTile] = lg2(fmaxf(v0[i], 5.42101086e-20f));  // 2^-64
+        at[2 * kTile] = v0[i] * kWeight;
+      }
+    }
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kPlaceThreads) : "memory");
+    arrive(&B->sc_full[slot]);
+    const int64_t* offs = s_off + slot * kTile;
+    const uint32_t kdst = smem_addr(smem + L::k + kr.slot * kKBytes);
+    const int ch = tid & 7;
+    if (ch < chunks) {
+      const uint8_t* base = static_cast<const uint8_t*>(P.c.k) + ch * 16;
+#pragma unroll
+      for (int i = 0; i < (kTile + kPlaceThreads / 8 - 1) / (kPlaceThreads / 8); ++i) {
+        const int t = (tid >> 3) + i * (kPlaceThreads / 8);
+        if (t < kTile) {
+          const int64_t off = offs[t];
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                       ::"r"(kdst + chunk_at(t, ch)), "l"(base + (off < 0 ? 0 : off)),
+                       "r"(off < 0 ? 0 : 16) : "memory");
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    // ---- V of the unit before, then this unit's loads
-    if (pending) convert();
+    if (u > 0) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      tc::fence_smem();
+      arrive(&B->k_full[kr.slot == 0 ? L::kK - 1 : kr.slot - 1]);
+    }
+    kr.next(L::kK);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  tc::fence_smem();
+  arrive(&B->k_full[kr.slot == 0 ? L::kK - 1 : kr.slot - 1]);
+}
+
+// 16 codes to 16 fp16; exact.
+__device__ __forceinline__ void to_f16(const uint4& c, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_f16x2(c.x), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y),
+                  e4m3x2_to_f16x2(c.y >> 16));
+  hi = make_uint4(e4m3x2_to_f16x2(c.z), e4m3x2_to_f16x2(c.z >> 16), e4m3x2_to_f16x2(c.w),
+                  e4m3x2_to_f16x2(c.w >> 16));
+}
+
+// Zeroes the NaN codes of a word; true if there were any.
+__device__ __forceinline__ bool drop_nans(uint32_t& w) {
+  const uint32_t hit = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+  w &= ~(hit * 255u);
+  return hit != 0u;
+}
+
+// Four warps: V, a unit ahead in registers, made fp16 on its way to shared
+// memory.  A thread has 16 channels (one 16-byte chunk) of 8 positions.
+template <int NS>
+__device__ __noinline__ void value_role(const AttendParams& P, int units, uint8_t* smem, Bars* B) {
+  using L = Plan<NS>;
+  const int tid = threadIdx.x & 127;
+  const int ch = tid & 7, t0 = tid >> 3;
+  const bool mine = ch < (P.c.head_dim >> 4);
+  const int64_t* s_off = reinterpret_cast<const int64_t*>(smem + L::off);
+  const uint8_t* src = static_cast<const uint8_t*>(P.c.v) + ch * 16;
+  // 32 bytes a position: chunks 2 (ch % 4) and the next of its half; the
+  // halves' lanes store them in opposite order, so that a quarter warp covers
+  // all banks.
+  const int swap = ch >> 2;
+  const uint32_t first = chunk_at(t0, (ch & 3) * 2 + swap) + (ch >> 2) * kVHalf;
+  const uint32_t other = chunk_at(t0, (ch & 3) * 2 + 1 - swap) + (ch >> 2) * kVHalf;
+  Ring vr, sr;
+  auto load = [&](int u, uint4 (&raw)[8]) {
+    wait(B, &B->sc_full[sr.slot], sr.phase);
+    sr.next(L::kSc);
+    const int64_t* offs = s_off + (u % L::kSc) * kTile + t0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t off = offs[16 * i];
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (off >= 0 && mine) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + off));
+    }
+  };
+  auto convert = [&](int u, uint4 (&raw)[8]) {
+    const int slot = u % L::kSc;
+    wait(B, &B->v_empty[vr.slot], vr.phase ^ 1u);
+    if (B->partial[slot] != 0) {
+      // A NaN that some row does not see: zero here, put back at the end.
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        nan |= drop_nans(raw[i].x);
+        nan |= drop_nans(raw[i].y);
+        nan |= drop_nans(raw[i].z);
+        nan |= drop_nans(raw[i].w);
+      }
+      if (nan) *reinterpret_cast<volatile int*>(&B->nan) = 1;
+    }
+    uint8_t* dst = smem + L::v + vr.slot * kVBytes;
     if (mine) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t off = offs[16 * i];
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (off >= 0)
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.c.v) + off + ch * 16));
+        uint4 lo, hi;
+        to_f16(raw[i], lo, hi);
+        // (16 positions on, the swizzle is the same.)
+        *reinterpret_cast<uint4*>(dst + first + i * 16 * 128) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + other + i * 16 * 128) = swap ? lo : hi;
       }
     }
-    {
-      // Whether every row of the block sees every position of this unit.
-      const int base = c.k.start + c.tile * kTile;
-      const int t_first = c.k.row0 / P.group, t_last = (c.k.row0 + c.k.rows - 1) / P.group;
-      int all_lo = c.r.begin;
-      if (P.window > 0) all_lo = max(all_lo, c.r.cached + t_last - P.window + 1);
-      pending_partial = base < all_lo || base + kTile - 1 > min(c.r.cached + t_first, c.k.end - 1);
-    }
-    pending = true;
-    pending_three = three;
-    asm volatile("cp.async.wait_all;" ::: "memory");
     tc::fence_smem();
-    mbar_arrive(&B->k_full[kr.slot]);
-    kr.next(L::kK);
-    three = next_three;
-    step(c);
+    arrive(&B->v_full[vr.slot]);
+    arrive(&B->sc_empty[slot]);
+    vr.next(L::kV);
+  };
+  uint4 r0[8], r1[8];
+  load(0, r0);
+  for (int u = 0; u < units; u += 2) {
+    if (u + 1 < units) load(u + 1, r1);
+    convert(u, r0);
+    if (u + 1 < units) {
+      if (u + 2 < units) load(u + 2, r0);
+      convert(u + 1, r1);
+    }
   }
-  if (pending) convert();
 }
 
 // ------------------------------------------------------------------ products
 
+// One whole warp, so that its operands stay in uniform registers; one elected
+// lane issues.
 template <int NS>
-__device__ void mma_role(const AttendParams& P, Cursor c, uint8_t* smem, Bars* B) {
+__device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* smem, Bars* B) {
   using L = Plan<NS>;
-  const uint32_t tmem = B->tmem;
+  const uint32_t tmem = __shfl_sync(kFull, B->tmem, 0);
   const int ksteps = (P.c.head_dim + 31) >> 5;
   const uint32_t qk_instr = tc::instruction(0, kTile, false);
-  const uint32_t pv_instr = tc::instruction(1, P.c.head_dim, true);
-  const uint32_t q0 = smem_addr(smem + L::q), k0 = smem_addr(smem + L::k), v0 = smem_addr(smem + L::v);
+  const uint32_t pv_instr = tc::instruction(0, P.c.head_dim, true);
+  constexpr uint32_t kHi = tc::operand_hi(1024);
+  const uint32_t q0 = tc::operand_lo(smem_addr(smem + L::q), 16);
+  const uint32_t k0 = tc::operand_lo(smem_addr(smem + L::k), 16);
+  const uint32_t v0 = tc::operand_lo(smem_addr(smem + L::v), kVHalf);
   Ring kr, vr;
-  uint32_t q_phase[2] = {0u, 0u}, p_phase[2] = {0u, 0u};
+  uint32_t q_phase = 0u, p_phase = 0u;  // bit t: tile t's
   auto qk = [&](int t) {
-    const uint64_t kd = tc::operand(k0 + kr.slot * kKBytes, 1024, 16);
+    const uint32_t kd = k0 + kr.slot * (kKBytes / 16), qd = q0 + t * (NS * kQBytes / 16);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint64_t qd = tc::operand(q0 + (t * NS + s) * kQBytes, 1024, 16);
-      for (int k = 0; k < ksteps; ++k)
-        tc::mma8_ss(tmem + t * kTile, qd + 2 * k, kd + 2 * k, qk_instr, s + k > 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < ksteps)
+          tc::mma8_ss(tmem + t * kTile, qd + s * (kQBytes / 16) + 2 * k, kd + 2 * k, kHi, qk_instr,
+                      s + k > 0);
+      }
     }
   };
   while (c.left > 0) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(c.k.tiles - c.tile), c.left));
-    const int tiles = c.k.rows > kTileRows ? 2 : 1;
-    wait(B, &B->k_full[kr.slot], kr.phase);
-    for (int t = 0; t < tiles; ++t) {
-      wait(B, &B->q_full[t], q_phase[t]);
-      q_phase[t] ^= 1u;
-      tc::fence_after();
-      qk(t);
-      tc::commit(&B->s_full[t]);
-    }
-    tc::commit(&B->k_empty[kr.slot]);
-    kr.next(L::kK);
-    for (int j = 0; j < n; ++j) {
-      const uint64_t vd = tc::operand(v0 + vr.slot * kVBytes, 1024, kVHalf);
-      for (int t = 0; t < tiles; ++t) {
-        wait(B, &B->p_full[t], p_phase[t]);
-        p_phase[t] ^= 1u;
-        if (t == 0) wait(B, &B->v_full[vr.slot], vr.phase);
-        tc::fence_after();
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc::mma16_ts(tmem + 256 + t * 128, tmem + t * kTile + 8 * k, vd + 128 * k, pv_instr,
-                       j + k > 0);
-        if (j + 1 < n) {
-          if (t == 0) wait(B, &B->k_full[kr.slot], kr.phase);
-          tc::fence_after();
-          qk(t);
-        }
-        tc::commit(&B->s_full[t]);
-      }
-      tc::commit(&B->v_empty[vr.slot]);
-      vr.next(L::kV);
-      if (j + 1 < n) {
-        tc::commit(&B->k_empty[kr.slot]);
-        kr.next(L::kK);
-      }
-    }
+    const int n = __shfl_sync(
+        kFull, static_cast<int>(min(static_cast<int64_t>(c.k.tiles - c.tile), c.left)), 0);
+    const int tiles = __shfl_sync(kFull, c.k.rows > kTileRows ? 2 : 1, 0);
     c.left -= n;
     if (c.left > 0) next_block(P, c, unit_shape());
+    wait(B, &B->k_full[kr.slot], kr.phase);
+    for (int t = 0; t < tiles; ++t) {
+      wait(B, &B->q_full[t], (q_phase >> t) & 1u);
+      q_phase ^= 1u << t;
+      tc::fence_after();
+      if (tc::elect()) {
+        qk(t);
+        tc::commit(&B->s_full[t]);
+        if (t == tiles - 1) tc::commit(&B->k_empty[kr.slot]);
+      }
+      __syncwarp();
+    }
+    kr.next(L::kK);
+    for (int j = 0; j < n; ++j) {
+      const uint32_t vd = v0 + vr.slot * (kVBytes / 16);
+      const bool more = j + 1 < n;
+      for (int t = 0; t < tiles; ++t) {
+        wait(B, &B->p_full[t], (p_phase >> t) & 1u);
+        p_phase ^= 1u << t;
+        if (t == 0) {
+          wait(B, &B->v_full[vr.slot], vr.phase);
+          if (more) wait(B, &B->k_full[kr.slot], kr.phase);
+        }
+        tc::fence_after();
+        if (tc::elect()) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc::mma16_ts(tmem + 256 + t * 128, tmem + t * kTile + 8 * k, vd + 128 * k, kHi, pv_instr,
+                         j + k > 0);
+          if (more) qk(t);
+          tc::commit(&B->s_full[t]);
+          if (t == tiles - 1) {
+            tc::commit(&B->v_empty[vr.slot]);
+            if (more) tc::commit(&B->k_empty[kr.slot]);
+          }
+        }
+        __syncwarp();
+      }
+      vr.next(L::kV);
+      if (more) kr.next(L::kK);
+    }
   }
 }
 
 // ------------------------------------------------------------------ softmax
 
+// One row's softmax of one unit: reads S, moves the running maximum m (and O
+// with it), adds to l, leaves P in S's place.  MASK: columns outside [from, to]
+// are not seen.  GROUPS: scales are the same over 16 columns.
+//
+// S is read twice, 64 columns at a time: all 128 scores of a row would not fit
+// its thread's registers.
+template <bool MASK, bool GROUPS>
+__device__ __forceinline__ void softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
+                                             int from, int to, float factor, int d, bool has_o,
+                                             float& m, float& l) {
+  uint32_t x[64];
+  auto mask = [&](int q) {
+    if (MASK) {
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        const int col = 64 * q + k;
+        if (col < from || col > to) x[k] = 0xff800000u;
+      }
+    }
+  };
+  // ---- the row's largest s + log2 vs
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    tc::ld64(s_tmem + 64 * q, x);
+    mask(q);
+    if (GROUPS) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float t = __uint_as_float(x[16 * g]), u = __uint_as_float(x[16 * g + 1]);
+#pragma unroll
+        for (int k = 2; k < 16; k += 4) {
+          t = max3(t, __uint_as_float(x[16 * g + k]), __uint_as_float(x[16 * g + k + 1]));
+          if (k + 3 < 16)
+            u = max3(u, __uint_as_float(x[16 * g + k + 2]), __uint_as_float(x[16 * g + k + 3]));
+        }
+        const int col = 64 * q + 16 * g;
+        most = fmaxf(most, fmaf(fmaxf(t, u), sc[col] * factor, sc[kTile + col]));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float4 ks = *reinterpret_cast<const float4*>(sc + 64 * q + k);
+        const float4 lv = *reinterpret_cast<const float4*>(sc + kTile + 64 * q + k);
+        const float a = fmaf(__uint_as_float(x[k]), ks.x * factor, lv.x);
+        const float b = fmaf(__uint_as_float(x[k + 1]), ks.y * factor, lv.y);
+        const float c = fmaf(__uint_as_float(x[k + 2]), ks.z * factor, lv.z);
+        const float e = fmaf(__uint_as_float(x[k + 3]), ks.w * factor, lv.w);
+        most = max3(most, max3(a, b, c), e);
+      }
+    }
+  }
+  const bool rise = most > m + kLazy;
+  if (__any_sync(kFull, rise)) {
+    const float now = rise ? most : m;
+    const float f = m == -INFINITY ? 0.0f : ex2(m - now);
+    m = now;
+    l *= f;
+    if (has_o) {
+#pragma unroll 1
+      for (int k = 0; k < d; k += 16) {
+        uint32_t o[16];
+        tc::ld16(o_tmem + k, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tc::st16(o_tmem + k, o);
+      }
+    }
+  }
+  // ---- weights
+  const float ref = m == -INFINITY ? 0.0f : m;
+  const uint64_t r2 = pack2(-ref, -ref);
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    tc::ld64(s_tmem + 64 * q, x);
+    mask(q);
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      uint64_t f0, f1, v0, v1;
+      const int col = 64 * q + 2 * i;
+      if (GROUPS) {
+        const int g = col & ~15;
+        const float f = sc[g] * factor, v = sc[2 * kTile + g];
+        f0 = f1 = pack2(f, f);
+        v0 = v1 = pack2(v, v);
+      } else {
+        const float4 ks = *reinterpret_cast<const float4*>(sc + col);
+        const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + col);
+        const uint64_t ff = pack2(factor, factor);
+        f0 = mul2(pack2(ks.x, ks.y), ff), f1 = mul2(pack2(ks.z, ks.w), ff);
+        v0 = pack2(vs.x, vs.y), v1 = pack2(vs.z, vs.w);
+      }
+      const float2 a = unpack2(
+          fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f0, r2));
+      const float2 b = unpack2(
+          fma2(pack2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3])), f1, r2));
+      const uint64_t wa = pack2(ex2(a.x), ex2(a.y)), wb = pack2(ex2(b.x), ex2(b.y));
+      sum[0] = add2(sum[0], wa);
+      sum[1] = add2(sum[1], wb);
+      const float2 pa = unpack2(mul2(wa, v0)), pb = unpack2(mul2(wb, v1));
+      p[i] = Pair<__half>::pack(pa.x, pa.y);
+      p[i + 1] = Pair<__half>::pack(pb.x, pb.y);
+    }
+    tc::st16(s_tmem + 32 * q, p);  // over columns that have been read
+    tc::st16(s_tmem + 32 * q + 16, p + 16);
+  }
+  const float2 s = unpack2(add2(sum[0], sum[1]));
+  l += s.x + s.y;
+}
+
 template <typename T, int NS>
-__device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range, uint8_t* smem,
+__device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const Range& range, uint8_t* smem,
                              Bars* B, int t) {
   using L = Plan<NS>;
   const int tid = threadIdx.x & 127, warp = tid >> 5;
@@ -390,6 +616,7 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
   const uint32_t o_tmem = s_tmem + 256;
   const int d = P.c.head_dim;
   const float* s_sc = reinterpret_cast<const float*>(smem + L::sc);
+  const bool groups = P.c.page_size % 16 == 0;
   uint32_t s_phase = 0u;
   Ring sr;
   while (c.left > 0) {
@@ -468,7 +695,7 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
       }
       tc::fence_smem();
       tc::fence_before();
-      mbar_arrive(&B->q_full[t]);
+      arrive(&B->q_full[t]);
     }
     // Positions that this row sees, and those that all rows of the tile see.
     const int pos = c.r.cached + tok;
@@ -490,75 +717,24 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
       // (After s_full, by when the scales are long there: a tile that skipped
       // blocks must not look at an earlier phase of this ring.)
       wait(B, &B->sc_full[sr.slot], sr.phase);
-      const float4* sc = reinterpret_cast<const float4*>(s_sc + sr.slot * kTile);
-      uint32_t u[kTile];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tc::ld32(s_tmem + 32 * k, u + 32 * k);
-      tc::wait_ld();
-#pragma unroll
-      for (int k = 0; k < kTile / 4; ++k) {
-        const float4 s4 = sc[k];
-        const float2 x = unpack2(mul2(pack2(__uint_as_float(u[4 * k]), __uint_as_float(u[4 * k + 1])),
-                                      pack2(s4.x, s4.y)));
-        const float2 y = unpack2(mul2(pack2(__uint_as_float(u[4 * k + 2]), __uint_as_float(u[4 * k + 3])),
-                                      pack2(s4.z, s4.w)));
-        u[4 * k] = __float_as_uint(x.x), u[4 * k + 1] = __float_as_uint(x.y);
-        u[4 * k + 2] = __float_as_uint(y.x), u[4 * k + 3] = __float_as_uint(y.y);
+      const float* sc = s_sc + sr.slot * 3 * kTile;
+      // (Copies of the code: a mask's comparisons cost as much as the rest of
+      // the arithmetic and few units need any; scales by group save a third.)
+      const int from = lo - base, to = hi - base;  // columns seen: [from, to]
+      const bool partial = base < all_lo || base + kTile - 1 > all_hi;
+      const int* mixed = B->mixed[sr.slot];
+      if (groups && (mixed[0] | mixed[1] | mixed[2]) == 0) {
+        if (partial)
+          softmax_unit<true, true>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
+        else
+          softmax_unit<false, true>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
+      } else {
+        softmax_unit<true, false>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
       }
       sr.next(L::kSc);
-      if (base < all_lo || base + kTile - 1 > all_hi) {
-        const int from = lo - base, to = hi - base;  // columns seen: [from, to]
-#pragma unroll
-        for (int k = 0; k < kTile; ++k)
-          if (k < from || k > to) u[k] = 0xff800000u;
-      }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < kTile; k += 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top[i] = fmaxf(fmaxf(top[i], __uint_as_float(u[k + 2 * i])), __uint_as_float(u[k + 2 * i + 1]));
-      }
-      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
-      const bool rise = most > m + kLazy;
-      if (__any_sync(kFull, rise)) {
-        const float now = rise ? most : m;
-        const float f = m == -INFINITY ? 0.0f : ex2(m - now);
-        m = now;
-        l *= f;
-        if (j > 0) {
-          for (int k = 0; k < d; k += 16) {
-            uint32_t o[16];
-            tc::ld16(o_tmem + k, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc::st16(o_tmem + k, o);
-          }
-        }
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      const uint64_t f2 = pack2(factor, factor), r2 = pack2(-ref, -ref);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = 32 * q + 2 * i;
-          const float2 x = unpack2(
-              fma2(pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), f2, r2));
-          const float a = ex2(x.x), b = ex2(x.y);
-          sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-          p[i] = Pair<__nv_bfloat16>::pack(a, b);
-        }
-        tc::st16(s_tmem + 16 * q, p);
-      }
-      const float2 s = unpack2(add2(sum[0], sum[1]));
-      l += s.x + s.y;
       tc::wait_st();
       tc::fence_before();
-      mbar_arrive(&B->p_full[t]);
+      arrive(&B->p_full[t]);
     }
     // ---- the block's end: O is complete
     wait(B, &B->s_full[t], s_phase);
@@ -593,11 +769,11 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
         P.lse[j_row * P.q_heads + h] = ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     };
     if (whole) {
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l != 0.0f ? (1.0f / kWeight) / l : 0.0f;
       for (int k = 0; k < d; k += 16) {
         uint32_t r[16];
+        __syncwarp();
         tc::ld16(o_tmem + k, r);
-        tc::wait_ld();
         float o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = l != 0.0f ? __uint_as_float(r[i]) : 0.0f;
@@ -618,8 +794,8 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
       float4* mine = reinterpret_cast<float4*>(partial(blockIdx.x));
       for (int k = 0; k < d; k += 16) {
         uint32_t r[16];
+        __syncwarp();
         tc::ld16(o_tmem + k, r);
-        tc::wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           __stcg(mine + (k / 4 + i) * kTileRows + tid,
@@ -656,7 +832,7 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
           const float2 s = stat(cta);
           ll += s.y * ex2(s.x - ref);
         }
-        const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+        const float inv = ll != 0.0f ? (1.0f / kWeight) / ll : 0.0f;
         for (int k = 0; k < d; k += 16) {
           float o[16];
 #pragma unroll
@@ -681,6 +857,7 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
         store_lse(mm, ll);
       }
     }
+    __syncwarp();
     tc::fence_before();  // O is read; the next block's products may overwrite it
     c.left -= n;
     if (c.left > 0) next_block(P, c, unit_shape());
@@ -688,11 +865,6 @@ __device__ void softmax_role(const AttendParams& P, Cursor c, const Range& range
 }
 
 // ------------------------------------------------------------------ kernel
-
-template <int R>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 template <typename T, int NS>
 __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
@@ -712,13 +884,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
     tc::fence_smem();
   }
   if (tid == 0) {
-    for (int i = 0; i < L::kK; ++i) mbar_init(&B->k_full[i], 128), mbar_init(&B->k_empty[i], 1);
-    for (int i = 0; i < L::kV; ++i) mbar_init(&B->v_full[i], 128), mbar_init(&B->v_empty[i], 1);
-    for (int i = 0; i < L::kSc; ++i) mbar_init(&B->sc_full[i], 128);
+    for (int i = 0; i < L::kK; ++i) mbar_init(&B->k_full[i], 3), mbar_init(&B->k_empty[i], 1);
+    for (int i = 0; i < L::kV; ++i) mbar_init(&B->v_full[i], 4), mbar_init(&B->v_empty[i], 1);
+    for (int i = 0; i < L::kSc; ++i) mbar_init(&B->sc_full[i], 3), mbar_init(&B->sc_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B->q_full[i], 128);
+      mbar_init(&B->q_full[i], 4);
       mbar_init(&B->s_full[i], 1);
-      mbar_init(&B->p_full[i], 128);
+      mbar_init(&B->p_full[i], 4);
     }
     B->dead = 0;
     B->nan = 0;
@@ -728,18 +900,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  // 512 threads of 128 registers: 2 * 176 + 104 + 56 = 4 * 128.
   if (warp < 8) {
-    regs_up<176>();
     softmax_role<T, NS>(P, c, range, smem, B, warp >> 2);
   } else if (warp < 12) {
-    regs_down<104>();
-    load_role<NS>(P, c, smem, B);
+    value_role<NS>(P, static_cast<int>(c.left), smem, B);
+  } else if (warp == 12) {
+    mma_role<NS>(P, c, smem, B);
   } else {
-    regs_down<56>();
-    if (tid == 12 * 32) mma_role<NS>(P, c, smem, B);
+    place_role<NS>(P, c, smem, B);
   }
   // Every product has been waited for (by the last block's softmax).
+  __syncwarp();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();

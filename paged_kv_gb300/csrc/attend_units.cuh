@@ -50,9 +50,11 @@ __device__ __forceinline__ Request load_request(const AttendParams& P, int i) {
 }
 
 // One block of rows: rows [row0, row0 + rows) of one request and cache head,
-// and the positions [start, end) that any of them sees.
+// and the positions [lo, end) that any of them sees.  Tiles begin at `start`,
+// the multiple of 16 at or below lo, so that groups of 16 positions lie within
+// pages of a multiple of 16 tokens.
 struct Block {
-  int row0, rows, start, end, tiles;
+  int row0, rows, start, lo, end, tiles;
 };
 
 __device__ __forceinline__ Block make_block(const AttendParams& P, const Request& r, int b,
@@ -63,9 +65,10 @@ __device__ __forceinline__ Block make_block(const AttendParams& P, const Request
   const int t0 = k.row0 / P.group, t1 = (k.row0 + k.rows - 1) / P.group;
   int lo = r.begin;
   if (P.window > 0) lo = max(lo, r.cached + t0 - P.window + 1);
-  k.start = lo;
+  k.lo = lo;
+  k.start = lo & ~15;
   k.end = r.end == 0 ? lo : r.cached + t1 + 1;
-  if (k.end < k.start) k.end = k.start;
+  if (k.end < k.lo) k.end = k.lo;
   k.tiles = max(1, (k.end - k.start + u.tile - 1) / u.tile);
   return k;
 }

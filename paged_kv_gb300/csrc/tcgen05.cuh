@@ -27,7 +27,6 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Orders this thread's shared-memory writes before reads by the tensor core.
 __device__ __forceinline__ void fence_smem() {
@@ -40,14 +39,26 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Shared-memory operand with the 128-byte swizzle (16-byte chunk c of 128-byte
-// row r at chunk c ^ (r % 8)), 1024-byte aligned groups of 8 rows.  `group` is
-// the byte distance of two groups; `wide` the distance of two 128-byte wide
-// columns of groups (operands whose contiguous dimension is not the summed one).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group, uint32_t wide) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) |
-         (static_cast<uint64_t>((wide >> 4) & 0x3fffu) << 16) |
-         (static_cast<uint64_t>((group >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok != 0u;
+}
+
+// A shared-memory operand's descriptor: 128-byte swizzle (16-byte chunk c of
+// 128-byte row r at chunk c ^ (r % 8)), 1024-byte aligned groups of 8 rows.
+// `group` is the byte distance of two groups; `wide` the distance of two
+// 128-byte wide columns of groups (operands whose contiguous dimension is not
+// the summed one).  The low word holds the address and `wide`, the high word
+// (the same for every operand of a kind) the rest; addresses advance by
+// adding bytes / 16 to the low word.
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t wide) {
+  return ((addr >> 4) & 0x3fffu) | (((wide >> 4) & 0x3fffu) << 16);
+}
+__host__ __device__ constexpr uint32_t operand_hi(uint32_t group) {
+  return ((group >> 4) & 0x3fffu) | (1u << 14) | (2u << 29);
 }
 
 // 128 x n product into fp32; types: 0 e4m3 (8 bits) or fp16, 1 bf16 (16 bits).
@@ -58,41 +69,52 @@ __host__ __device__ constexpr uint32_t instruction(int type, int n, bool b_wide)
 }
 
 // d (+)= a b^T, 8-bit operands, 32 summed elements, both in shared memory.
-__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                        uint32_t instr, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(add ? 1u : 0u) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}"
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(instr), "r"(add ? 1u : 0u) : "memory");
 }
 // d (+)= a b, 16-bit operands, 16 summed elements, a in tensor memory.
-__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool add) {
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                         uint32_t instr, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(instr), "r"(add ? 1u : 0u) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(instr), "r"(add ? 1u : 0u) : "memory");
 }
 
-// 32 columns of this warp's 32 lanes (one row a thread).
-__device__ __forceinline__ void ld32(uint32_t addr, uint32_t* r) {
+// Loads come with their wait in one statement: between the two the registers
+// must not be touched, not even moved or spilled by the compiler.
+//
+// 64 columns of this warp's 32 lanes (one row a thread).
+__device__ __forceinline__ void ld64(uint32_t addr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32,"
+      " %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48,"
+      " %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void ld16(uint32_t addr, uint32_t* r) {
+__device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
