@@ -9,13 +9,13 @@
 //     (elements below 2^-9 of a row's largest keep an absolute 2^-17 of it);
 //   S times the page's key scale and the row's factor, softmax in fp32;
 //   O[128 x D] += P V      on kind::f16: V's codes made fp16 (exactly) on their
-//     way to shared memory, P = 2^7 2^(s - m) vs in fp16 in tensor memory, in
+//     way to shared memory, P = 2^3 2^(s - m) vs in fp16 in tensor memory, in
 //     S's place, with the page's value scale in it and m the running maximum
-//     of s + log2 vs.  m moves only when it would rise by more than 8, so P
-//     stays below 2^15 and keeps fp16's 11 bits down to 2^-22 of the largest:
-//     a long context's weights may lie far below an early large one and still
-//     add up to as much.  l sums 2^(s - m) in fp32.
-// When m moves, O is rescaled in tensor memory by the row's own thread.
+//     of s + log2 vs.  m moves only when it would rise by more than 12, so P
+//     stays below 2^15 and keeps fp16's 11 bits down to 2^-17 of the largest
+//     weight and some bits down to 2^-27: a long context's weights may lie far
+//     below an early large one and still add up.  l sums 2^(s - m) in fp32.
+// When m moves, O is rescaled in tensor memory by the rows' own threads.
 //
 // Roles (16 warps): warps 0-3 and 4-7 are the softmax of tile 0 and 1, a
 // thread a row; warps 8-11 bring V, converting it in registers; warp 12 issues
@@ -28,12 +28,9 @@
 // Products of one thread run in issue order, so P V and the next Q K^T of a
 // tile, which writes over P, need no barrier between them.
 //
-// Every wait ends: after kWaitNs a thread sets `dead`, with which all waits
+// Every wait ends: after kWaitTries a thread sets `dead`, with which all waits
 // return at once, the loops (whose lengths do not depend on data) run out,
 // tensor memory is freed and PKV_ST_TIMEOUT is set.
-//
-// Bound: instruction issue of the softmax and conversion warps (about 1500
-// issue cycles per SM quarter a unit against 1024 tensor cycles).
 
 #include <cuda_runtime.h>
 
@@ -63,10 +60,10 @@ constexpr int kQBytes = kTileRows * kPitch;
 constexpr int kKBytes = kTile * kPitch;
 constexpr int kVHalf = kTile * 128;      // 64 channels of bf16
 constexpr int kVBytes = 2 * kVHalf;
-constexpr float kLazy = 8.0f;
-constexpr float kWeight = 128.0f;        // weights are this times 2^(s - m) vs
+constexpr float kLazy = 12.0f;
+constexpr float kWeight = 8.0f;          // weights are this times 2^(s - m) vs
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr long long kWaitNs = 2000000000ll;
+constexpr int kWaitTries = 1 << 20;
 __host__ __device__ constexpr UnitShape unit_shape() {
   return UnitShape{kBlockRows, kTile, kRowLimit + 1, int64_t{1} << 40};
 }
@@ -80,7 +77,8 @@ struct Plan {
   static constexpr int k = q + 2 * NS * kQBytes;
   static constexpr int v = k + kK * kKBytes;
   static constexpr int sc = v + kV * kVBytes;        // scales, kSc slots: ks, log2 vs, vs
-  static constexpr int off = sc + kSc * 3 * kTile * 4;  // byte offsets
+  static constexpr int gr = sc + kSc * 3 * kTile * 4;   // the same of each group of 16
+  static constexpr int off = gr + kSc * 8 * 16;         // byte offsets
   static constexpr int bar = off + kSc * kTile * 8;
   static constexpr int bytes = bar + 512 + 1024;     // and room to align
 };
@@ -105,19 +103,24 @@ struct Ring {
   }
 };
 
+// The rest of a wait: the hardware suspends the thread between tries.
+__device__ __noinline__ void wait_more(Bars* B, uint64_t* bar, uint32_t parity) {
+  for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
+    if (i == kWaitTries) *reinterpret_cast<volatile int*>(&B->dead) = 1;
+    if (*reinterpret_cast<volatile int*>(&B->dead) != 0) break;
+  }
+}
+
 // By whole warps, which leave it converged: what follows may be an instruction
 // that all lanes have to issue together.
 __device__ __forceinline__ void wait(Bars* B, uint64_t* bar, uint32_t parity) {
-  if (!mbar_try_wait(bar, parity)) {
-    const long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-      if (*reinterpret_cast<volatile int*>(&B->dead) != 0) break;
-      if (globaltimer_ns() - t0 > kWaitNs) {
-        *reinterpret_cast<volatile int*>(&B->dead) = 1;
-        break;
-      }
-    }
-  }
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+  if (!__all_sync(kFull, ok != 0u)) wait_more(B, bar, parity);
   __syncwarp();
 }
 
@@ -127,10 +130,10 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-template <int ID>
-__device__ __forceinline__ void bar_sync(int id_add = 0) {
+// The 128 softmax threads of tile t.
+__device__ __forceinline__ void tile_sync(int t) {
   __syncwarp();
-  asm volatile("bar.sync %0, 128;" ::"r"(ID + id_add) : "memory");
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -194,13 +197,14 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
   const int slots = static_cast<int>(P.c.num_pages * P.c.page_size);
   const int chunks = P.c.head_dim >> 4;
   float* s_sc = reinterpret_cast<float*>(smem + L::sc);
+  float4* s_gr = reinterpret_cast<float4*>(smem + L::gr);
   int64_t* s_off = reinterpret_cast<int64_t*>(smem + L::off);
   constexpr int kPer = 2;
   const bool second = tid + kPlaceThreads < kTile;
 
   // A place outside the block's positions takes the nearest one's location, for
   // its scales alone; loc -1: outside the cache, or no position at all.
-  struct Places { int loc[kPer]; bool in[kPer]; int head; bool partial; };
+  struct Places { int loc[kPer]; bool in[kPer]; bool some, partial; int head; };
   int all_lo = 0, all_hi = 0;
   auto block_bounds = [&]() {  // positions that every row of the block sees
     const int t_first = a.k.row0 / P.group, t_last = (a.k.row0 + a.k.rows - 1) / P.group;
@@ -212,7 +216,7 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
   auto read_places = [&]() -> Places {
     Places p;
     p.loc[0] = p.loc[1] = -1;
-    p.in[0] = p.in[1] = false;
+    p.in[0] = p.in[1] = p.some = false;
     p.head = 0;
     p.partial = false;
     if (a.left > 0) {
@@ -224,11 +228,8 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
         if (a.k.lo < a.k.end && (i == 0 || second)) {
           const int near = max(a.k.lo, min(tok, a.k.end - 1));
           p.in[i] = near == tok;
-          p.loc[i] = row[near];
-          if (p.loc[i] < 0 || p.loc[i] >= slots) {
-            if (P.status != nullptr) atomicOr(P.status, PKV_ST_ROW_OOB);
-            p.loc[i] = -1;
-          }
+          p.some = true;
+          p.loc[i] = row[near];  // not looked at before resolve()
         }
       }
       p.head = a.head;
@@ -250,7 +251,10 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
       int page = -1;
       ks[i] = 1.0f;  // (of a zero key; it must not turn a masked -inf into NaN)
       vs[i] = 0.0f;
-      if (p.loc[i] >= 0) {
+      const bool mine = p.some && (i == 0 || second);
+      if (mine && (p.loc[i] < 0 || p.loc[i] >= slots)) {
+        if (P.status != nullptr) atomicOr(P.status, PKV_ST_ROW_OOB);
+      } else if (mine) {
         page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(p.loc[i])));
         if (p.in[i])
           off = page * P.c.page_stride + (p.loc[i] - page * P.c.page_size) * P.c.token_stride +
@@ -290,10 +294,13 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (i == 0 || second) {
-        float* at = s_sc + slot * 3 * kTile + tid + i * kPlaceThreads;
+        const int tok = tid + i * kPlaceThreads;
+        float* at = s_sc + slot * 3 * kTile + tok;
+        const float lv = lg2(fmaxf(v0[i], 5.42101086e-20f)), vw = v0[i] * kWeight;  // 2^-64
         at[0] = k0[i];
-        at[kTile] = lg2(fmaxf(v0[i], 5.42101086e-20f));  // 2^-64
-        at[2 * kTile] = v0[i] * kWeight;
+        at[kTile] = lv;
+        at[2 * kTile] = vw;
+        if ((tok & 15) == 0) s_gr[slot * 8 + (tok >> 4)] = make_float4(k0[i], lv, vw, 0.0f);
       }
     }
     __syncwarp();
@@ -457,6 +464,7 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
       if (tc::elect()) {
         qk(t);
         tc::commit(&B->s_full[t]);
+        mbar_arrive(&B->s_full[t]);
         if (t == tiles - 1) tc::commit(&B->k_empty[kr.slot]);
       }
       __syncwarp();
@@ -466,12 +474,12 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
       const uint32_t vd = v0 + vr.slot * (kVBytes / 16);
       const bool more = j + 1 < n;
       for (int t = 0; t < tiles; ++t) {
-        wait(B, &B->p_full[t], (p_phase >> t) & 1u);
-        p_phase ^= 1u << t;
         if (t == 0) {
           wait(B, &B->v_full[vr.slot], vr.phase);
           if (more) wait(B, &B->k_full[kr.slot], kr.phase);
         }
+        wait(B, &B->p_full[t], (p_phase >> t) & 1u);
+        p_phase ^= 1u << t;
         tc::fence_after();
         if (tc::elect()) {
 #pragma unroll
@@ -480,6 +488,7 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
                          j + k > 0);
           if (more) qk(t);
           tc::commit(&B->s_full[t]);
+          mbar_arrive(&B->s_full[t]);
           if (t == tiles - 1) {
             tc::commit(&B->v_empty[vr.slot]);
             if (more) tc::commit(&B->k_empty[kr.slot]);
@@ -495,50 +504,62 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
 
 // ------------------------------------------------------------------ softmax
 
+// Moves a row's reference by a factor f of its O.  (A function of its own, as
+// are the rarer forms of the softmax below: the loop that runs for every unit
+// stays small enough for the instruction caches.)
+__device__ __noinline__ void rescale(uint32_t o_tmem, int d, float f) {
+#pragma unroll 1
+  for (int k = 0; k < d; k += 32) {
+    uint32_t o[32];
+    tc::ld32(o_tmem + k, o);  // (past d: columns that nothing reads)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    tc::st16(o_tmem + k, o);
+    tc::st16(o_tmem + k + 16, o + 16);
+  }
+}
+
 // One row's softmax of one unit: reads S, moves the running maximum m (and O
 // with it), adds to l, leaves P in S's place.  MASK: columns outside [from, to]
 // are not seen.  GROUPS: scales are the same over 16 columns.
 //
-// S is read twice, 64 columns at a time: all 128 scores of a row would not fit
-// its thread's registers.
+// S is read twice, 32 columns at a time: more would not fit the registers.
 template <bool MASK, bool GROUPS>
-__device__ __forceinline__ void softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
-                                             int from, int to, float factor, int d, bool has_o,
-                                             float& m, float& l) {
-  uint32_t x[64];
-  auto mask = [&](int q) {
+__device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
+                                               const float4* gr, int from, int to, float factor,
+                                               int o_cols, float m, float l) {
+  auto mask = [&](uint32_t (&x)[32], int q) {
     if (MASK) {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        const int col = 64 * q + k;
-        if (col < from || col > to) x[k] = 0xff800000u;
-      }
+      for (int k = 0; k < 32; ++k)
+        if (32 * q + k < from || 32 * q + k > to) x[k] = 0xff800000u;
     }
   };
   // ---- the row's largest s + log2 vs
   float most = -INFINITY;
 #pragma unroll 1
-  for (int q = 0; q < 2; ++q) {
-    tc::ld64(s_tmem + 64 * q, x);
-    mask(q);
+  for (int q = 0; q < kTile / 32; ++q) {
+    uint32_t x[32];
+    tc::ld32(s_tmem + 32 * q, x);
+    mask(x, q);
     if (GROUPS) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float t = __uint_as_float(x[16 * g]), u = __uint_as_float(x[16 * g + 1]);
+      for (int g = 0; g < 2; ++g) {
+        const float4 scale = gr[2 * q + g];
+        float a = __uint_as_float(x[16 * g]), b = __uint_as_float(x[16 * g + 1]);
 #pragma unroll
         for (int k = 2; k < 16; k += 4) {
-          t = max3(t, __uint_as_float(x[16 * g + k]), __uint_as_float(x[16 * g + k + 1]));
+          a = max3(a, __uint_as_float(x[16 * g + k]), __uint_as_float(x[16 * g + k + 1]));
           if (k + 3 < 16)
-            u = max3(u, __uint_as_float(x[16 * g + k + 2]), __uint_as_float(x[16 * g + k + 3]));
+            b = max3(b, __uint_as_float(x[16 * g + k + 2]), __uint_as_float(x[16 * g + k + 3]));
         }
-        const int col = 64 * q + 16 * g;
-        most = fmaxf(most, fmaf(fmaxf(t, u), sc[col] * factor, sc[kTile + col]));
+        most = fmaxf(most, fmaf(fmaxf(a, b), scale.x * factor, scale.y));
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 64; k += 4) {
-        const float4 ks = *reinterpret_cast<const float4*>(sc + 64 * q + k);
-        const float4 lv = *reinterpret_cast<const float4*>(sc + kTile + 64 * q + k);
+      for (int k = 0; k < 32; k += 4) {
+        const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * q + k);
+        const float4 lv = *reinterpret_cast<const float4*>(sc + kTile + 32 * q + k);
         const float a = fmaf(__uint_as_float(x[k]), ks.x * factor, lv.x);
         const float b = fmaf(__uint_as_float(x[k + 1]), ks.y * factor, lv.y);
         const float c = fmaf(__uint_as_float(x[k + 2]), ks.z * factor, lv.z);
@@ -553,78 +574,123 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_tmem, uint32_t o_tmem, c
     const float f = m == -INFINITY ? 0.0f : ex2(m - now);
     m = now;
     l *= f;
-    if (has_o) {
-#pragma unroll 1
-      for (int k = 0; k < d; k += 16) {
-        uint32_t o[16];
-        tc::ld16(o_tmem + k, o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-        tc::st16(o_tmem + k, o);
-      }
-    }
+    if (o_cols > 0) rescale(o_tmem, o_cols, f);
   }
   // ---- weights
   const float ref = m == -INFINITY ? 0.0f : m;
   const uint64_t r2 = pack2(-ref, -ref);
   uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
-  for (int q = 0; q < 2; ++q) {
-    tc::ld64(s_tmem + 64 * q, x);
-    mask(q);
-    uint32_t p[32];
+  for (int q = 0; q < kTile / 32; ++q) {
+    uint32_t x[32], p[16];
+    tc::ld32(s_tmem + 32 * q, x);
+    mask(x, q);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      uint64_t f0, f1, v0, v1;
-      const int col = 64 * q + 2 * i;
-      if (GROUPS) {
-        const int g = col & ~15;
-        const float f = sc[g] * factor, v = sc[2 * kTile + g];
-        f0 = f1 = pack2(f, f);
-        v0 = v1 = pack2(v, v);
-      } else {
-        const float4 ks = *reinterpret_cast<const float4*>(sc + col);
-        const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + col);
-        const uint64_t ff = pack2(factor, factor);
-        f0 = mul2(pack2(ks.x, ks.y), ff), f1 = mul2(pack2(ks.z, ks.w), ff);
-        v0 = pack2(vs.x, vs.y), v1 = pack2(vs.z, vs.w);
+    for (int g = 0; g < 2; ++g) {
+      float4 scale;
+      if (GROUPS) scale = gr[2 * q + g];
+      const float fg = scale.x * factor;
+      const uint64_t fg2 = pack2(fg, fg), vg2 = pack2(scale.z, scale.z);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        uint64_t f0 = fg2, f1 = fg2, v0 = vg2, v1 = vg2;
+        const int col = 16 * g + i;
+        if (!GROUPS) {
+          const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * q + col);
+          const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + 32 * q + col);
+          const uint64_t ff = pack2(factor, factor);
+          f0 = mul2(pack2(ks.x, ks.y), ff), f1 = mul2(pack2(ks.z, ks.w), ff);
+          v0 = pack2(vs.x, vs.y), v1 = pack2(vs.z, vs.w);
+        }
+        const float2 a = unpack2(
+            fma2(pack2(__uint_as_float(x[col]), __uint_as_float(x[col + 1])), f0, r2));
+        const float2 b = unpack2(
+            fma2(pack2(__uint_as_float(x[col + 2]), __uint_as_float(x[col + 3])), f1, r2));
+        const uint64_t wa = pack2(ex2(a.x), ex2(a.y)), wb = pack2(ex2(b.x), ex2(b.y));
+        sum[0] = add2(sum[0], wa);
+        sum[1] = add2(sum[1], wb);
+        const float2 pa = unpack2(mul2(wa, v0)), pb = unpack2(mul2(wb, v1));
+        p[col / 2] = Pair<__half>::pack(pa.x, pa.y);
+        p[col / 2 + 1] = Pair<__half>::pack(pb.x, pb.y);
       }
-      const float2 a = unpack2(
-          fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f0, r2));
-      const float2 b = unpack2(
-          fma2(pack2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3])), f1, r2));
-      const uint64_t wa = pack2(ex2(a.x), ex2(a.y)), wb = pack2(ex2(b.x), ex2(b.y));
-      sum[0] = add2(sum[0], wa);
-      sum[1] = add2(sum[1], wb);
-      const float2 pa = unpack2(mul2(wa, v0)), pb = unpack2(mul2(wb, v1));
-      p[i] = Pair<__half>::pack(pa.x, pa.y);
-      p[i + 1] = Pair<__half>::pack(pb.x, pb.y);
     }
-    tc::st16(s_tmem + 32 * q, p);  // over columns that have been read
-    tc::st16(s_tmem + 32 * q + 16, p + 16);
+    tc::st16(s_tmem + 16 * q, p);  // over columns that have been read
   }
   const float2 s = unpack2(add2(sum[0], sum[1]));
-  l += s.x + s.y;
+  return make_float2(m, l + (s.x + s.y));
+}
+
+template <bool GROUPS>
+__device__ __noinline__ float2 softmax_masked(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
+                                              const float4* gr, int from, int to, float factor,
+                                              int o_cols, float m, float l) {
+  return softmax_unit<true, GROUPS>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
+}
+
+// What a block's units need of one softmax thread.
+struct RowState {
+  float m, l;
+  uint32_t unit;      // units before this one in the CTA's range
+  uint32_t s_phase;
+};
+
+// The softmax of one row over `n` units.
+//   from, to: columns of the first unit that the row sees, going down by kTile
+//   a unit; all_from, all_to: those that every row of the tile sees;
+//   tile: bit 0 the tile, bit 1 scales by groups may be used.
+__device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float* s_sc,
+                                               const float4* s_gr, uint32_t s_tmem, uint32_t o_tmem,
+                                               float factor, int d, int n, int from, int to,
+                                               int all_from, int all_to, int tile) {
+  const int t = tile & 1;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const uint32_t slot = r.unit % Plan<2>::kSc;
+    wait(B, &B->s_full[t], r.s_phase);  // (and the unit's scales with it)
+    r.s_phase ^= 1u;
+    tc::fence_after();
+    const float4* gr = s_gr + slot * 8;
+    const int cols = j > 0 ? d : 0;
+    const int* mixed = B->mixed[slot];
+    const bool groups = (tile & 2) != 0 && (mixed[0] | mixed[1] | mixed[2]) == 0;
+    float2 ml;
+    if (groups && all_from <= 0 && all_to >= kTile - 1) {
+      ml = softmax_unit<false, true>(s_tmem, o_tmem, nullptr, gr, 0, 0, factor, cols, r.m, r.l);
+    } else {
+      const float* sc = s_sc + slot * 3 * kTile;
+      ml = groups ? softmax_masked<true>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
+                  : softmax_masked<false>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
+    }
+    r.m = ml.x;
+    r.l = ml.y;
+    tc::wait_st();
+    tc::fence_before();
+    arrive(&B->p_full[t]);
+    ++r.unit;
+    from -= kTile, to -= kTile, all_from -= kTile, all_to -= kTile;
+  }
+  return r;
 }
 
 template <typename T, int NS>
-__device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const Range& range, uint8_t* smem,
-                             Bars* B, int t) {
+__device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const Range& range,
+                                          uint8_t* smem, Bars* B, int t) {
   using L = Plan<NS>;
-  const int tid = threadIdx.x & 127, warp = tid >> 5;
-  const uint32_t s_tmem = B->tmem + (static_cast<uint32_t>(warp * 32) << 16) + t * kTile;
-  const uint32_t o_tmem = s_tmem + 256;
+  static_assert(L::kSc == Plan<2>::kSc, "one ring size");
+  const int tid = threadIdx.x & 127, warp = tid >> 5;  // tid: the row of the tile
   const int d = P.c.head_dim;
+  const uint32_t lanes = B->tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const uint32_t s_tmem = lanes + t * kTile, o_tmem = s_tmem + 256;
   const float* s_sc = reinterpret_cast<const float*>(smem + L::sc);
-  const bool groups = P.c.page_size % 16 == 0;
-  uint32_t s_phase = 0u;
-  Ring sr;
+  const float4* s_gr = reinterpret_cast<const float4*>(smem + L::gr);
+  const int tile = t + (P.c.page_size % 16 == 0 ? 2 : 0);
+  RowState st{0.0f, 0.0f, 0u, 0u};
   while (c.left > 0) {
     const int t_begin = c.tile;
     const int n = static_cast<int>(min(static_cast<int64_t>(c.k.tiles - c.tile), c.left));
     const bool whole = n == c.k.tiles;
     if (t == 1 && c.k.rows <= kTileRows) {  // nothing for this tile
-      for (int j = 0; j < n; ++j) sr.next(L::kSc);
+      st.unit += n;
       c.left -= n;
       if (c.left > 0) next_block(P, c, unit_shape());
       continue;
@@ -632,15 +698,16 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
     const int row = t * kTileRows + tid;  // of the block
     const int tok = (c.k.row0 + row) / P.group, g = c.k.row0 + row - tok * P.group;
     const int64_t j_row = c.q_off + tok;
-    const int h = c.head * P.group + g;
+    const int head = c.head * P.group + g;
     const bool live = row < c.k.rows;
     const bool there = live && j_row < P.n_tokens;
     // ---- the row's query as NS e4m3 rows
     float factor;  // score (log2) of a product of codes
     {
-      const uint16_t* src = P.q + j_row * P.q_ts + static_cast<int64_t>(h) * P.q_hs;
+      const uint16_t* src = P.q + j_row * P.q_ts + static_cast<int64_t>(head) * P.q_hs;
       float amax = 0.0f;
       if (there) {
+#pragma unroll 4
         for (int i = 0; i < d; i += 8) {
           const uint4 x = *reinterpret_cast<const uint4*>(src + i);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -659,15 +726,14 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       factor = fmaxf(fabsf(P.scale_log2) / unit, 1.17549435e-38f);  // -inf stays -inf
       const float sign = P.scale_log2 < 0.0f ? -unit : unit;
       uint8_t* q = smem + L::q + t * NS * kQBytes;
+#pragma unroll 1
       for (int i = 0; i < d; i += 16) {
-        uint32_t w[8];
         uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
         if (there) {
           x = *reinterpret_cast<const uint4*>(src + i);
           y = *reinterpret_cast<const uint4*>(src + i + 8);
         }
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         float v[16];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -702,46 +768,25 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
     int lo = c.r.begin;
     if (P.window > 0) lo = max(lo, pos - P.window + 1);
     const int hi = min(pos, c.k.end - 1);
-    const int first_row = c.k.row0 + t * kTileRows;
-    const int last_row = c.k.row0 + min(c.k.rows, (t + 1) * kTileRows) - 1;
-    const int all_hi = min(c.r.cached + first_row / P.group, c.k.end - 1);
-    int all_lo = c.r.begin;
-    if (P.window > 0) all_lo = max(all_lo, c.r.cached + last_row / P.group - P.window + 1);
-
-    float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j < n; ++j) {
-      const int base = c.k.start + (t_begin + j) * kTile;
-      wait(B, &B->s_full[t], s_phase);
-      s_phase ^= 1u;
-      tc::fence_after();
-      // (After s_full, by when the scales are long there: a tile that skipped
-      // blocks must not look at an earlier phase of this ring.)
-      wait(B, &B->sc_full[sr.slot], sr.phase);
-      const float* sc = s_sc + sr.slot * 3 * kTile;
-      // (Copies of the code: a mask's comparisons cost as much as the rest of
-      // the arithmetic and few units need any; scales by group save a third.)
-      const int from = lo - base, to = hi - base;  // columns seen: [from, to]
-      const bool partial = base < all_lo || base + kTile - 1 > all_hi;
-      const int* mixed = B->mixed[sr.slot];
-      if (groups && (mixed[0] | mixed[1] | mixed[2]) == 0) {
-        if (partial)
-          softmax_unit<true, true>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
-        else
-          softmax_unit<false, true>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
-      } else {
-        softmax_unit<true, false>(s_tmem, o_tmem, sc, from, to, factor, d, j > 0, m, l);
-      }
-      sr.next(L::kSc);
-      tc::wait_st();
-      tc::fence_before();
-      arrive(&B->p_full[t]);
+    {
+      const int first_row = c.k.row0 + t * kTileRows;
+      const int last_row = c.k.row0 + min(c.k.rows, (t + 1) * kTileRows) - 1;
+      const int all_hi = min(c.r.cached + first_row / P.group, c.k.end - 1);
+      int all_lo = c.r.begin;
+      if (P.window > 0) all_lo = max(all_lo, c.r.cached + last_row / P.group - P.window + 1);
+      const int base = c.k.start + t_begin * kTile;
+      st.m = -INFINITY;
+      st.l = 0.0f;
+      st = softmax_units(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
+                         all_lo - base, all_hi - base, tile);
     }
     // ---- the block's end: O is complete
-    wait(B, &B->s_full[t], s_phase);
-    s_phase ^= 1u;
+    wait(B, &B->s_full[t], st.s_phase);
+    st.s_phase ^= 1u;
     tc::fence_after();
+    const float m = st.m, l = st.l;
     bool nan = *reinterpret_cast<volatile int*>(&B->nan) != 0;
-    const int64_t out_at = j_row * P.o_ts + static_cast<int64_t>(h) * P.o_hs;
+    const int64_t out_at = j_row * P.o_ts + static_cast<int64_t>(head) * P.o_hs;
     // NaN codes of partly seen units were left out of the products.
     auto put_nans = [&](int k, float (&o)[16]) {
       for (int p = lo; p <= hi && p < c.k.end; ++p) {
@@ -766,10 +811,11 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
     };
     auto store_lse = [&](float mm, float ll) {
       if (P.lse != nullptr)
-        P.lse[j_row * P.q_heads + h] = ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+        P.lse[j_row * P.q_heads + head] = ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     };
     if (whole) {
       const float inv = l != 0.0f ? (1.0f / kWeight) / l : 0.0f;
+#pragma unroll 1
       for (int k = 0; k < d; k += 16) {
         uint32_t r[16];
         __syncwarp();
@@ -792,9 +838,9 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         return P.partials + at * size;
       };
       float4* mine = reinterpret_cast<float4*>(partial(blockIdx.x));
+#pragma unroll 1
       for (int k = 0; k < d; k += 16) {
         uint32_t r[16];
-        __syncwarp();
         tc::ld16(o_tmem + k, r);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -806,7 +852,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       __stcg(stats + tid, make_float2(m, l));
       if (tid == 0) __stcg(stats + kTileRows, make_float2(nan ? 1.0f : 0.0f, 0.0f));
       __threadfence();
-      bar_sync<2>(t);
+      tile_sync(t);
       if (tid == 0) {
         uint32_t* counter = P.counters + 2 * c0 + t;
         const bool is_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(c1 - c0);
@@ -814,41 +860,46 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         __threadfence();
         *reinterpret_cast<volatile int*>(&B->last[t]) = is_last ? 1 : 0;
       }
-      bar_sync<2>(t);
+      tile_sync(t);
       if (*reinterpret_cast<volatile int*>(&B->last[t]) != 0 && there) {
         // Joined in CTA order.
         auto stat_of = [&](int64_t cta, int i) {
           return __ldcg(
               reinterpret_cast<const float2*>(partial(cta) + static_cast<int64_t>(kTileRows) * d) + i);
         };
-        auto stat = [&](int64_t cta) { return stat_of(cta, tid); };
         float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 4
         for (int64_t cta = c0; cta <= c1; ++cta) {
-          mm = fmaxf(mm, stat(cta).x);
+          mm = fmaxf(mm, stat_of(cta, tid).x);
           nan = nan || stat_of(cta, kTileRows).x != 0.0f;
         }
         const float ref = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll 4
         for (int64_t cta = c0; cta <= c1; ++cta) {
-          const float2 s = stat(cta);
+          const float2 s = stat_of(cta, tid);
           ll += s.y * ex2(s.x - ref);
         }
         const float inv = ll != 0.0f ? (1.0f / kWeight) / ll : 0.0f;
+#pragma unroll 1
         for (int k = 0; k < d; k += 16) {
           float o[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+#pragma unroll 2
           for (int64_t cta = c0; cta <= c1; ++cta) {
-            const float2 s = stat(cta);
-            if (s.y == 0.0f) continue;  // that part saw nothing
+            const float2 s = stat_of(cta, tid);
             const float f = ex2(s.x - ref);
-            const float4* p = reinterpret_cast<const float4*>(partial(cta));
+            const float4* p = reinterpret_cast<const float4*>(partial(cta)) + (k / 4) * kTileRows + tid;
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __ldcg(p + i * kTileRows);
+            if (s.y == 0.0f) continue;  // that part saw nothing
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float4 x = __ldcg(p + (k / 4 + i) * kTileRows + tid);
-              o[4 * i] = fmaf(x.x, f, o[4 * i]);
-              o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
+              o[4 * i] = fmaf(x[i].x, f, o[4 * i]);
+              o[4 * i + 1] = fmaf(x[i].y, f, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(x[i].z, f, o[4 * i + 2]);
+              o[4 * i + 3] = fmaf(x[i].w, f, o[4 * i + 3]);
             }
           }
           if (nan) put_nans(k, o);
@@ -889,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
     for (int i = 0; i < L::kSc; ++i) mbar_init(&B->sc_full[i], 3), mbar_init(&B->sc_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->q_full[i], 4);
-      mbar_init(&B->s_full[i], 1);
+      mbar_init(&B->s_full[i], 2);
       mbar_init(&B->p_full[i], 4);
     }
     B->dead = 0;
