@@ -8,14 +8,14 @@
 //     rows, exactly: 4 significant bits each, so 2 for bf16 and 3 for fp16
 //     (elements below 2^-9 of a row's largest keep an absolute 2^-17 of it);
 //   S times the page's key scale and the row's factor, softmax in fp32;
-//   O[128 x D] += P V      on kind::f16: V's codes made fp16 (exactly) on their
-//     way to shared memory, P = 2^3 2^(s - m) vs in fp16 in tensor memory, in
-//     S's place, with the page's value scale in it and m the running maximum
-//     of s + log2 vs.  m moves only when it would rise by more than 12, so P
-//     stays below 2^15 and keeps fp16's 11 bits down to 2^-17 of the largest
-//     weight and some bits down to 2^-27: a long context's weights may lie far
-//     below an early large one and still add up.  l sums 2^(s - m) in fp32.
-// When m moves, O is rescaled in tensor memory by the rows' own threads.
+//   O[128 x D] += P V      on kind::f16: V's codes made 16 bits wide (exactly) on
+//     their way to shared memory, P = 2^(s - m) vs in tensor memory, in S's
+//     place, with the page's value scale in it.  l sums 2^(s - m) in fp32.
+// P and V take the queries' type.  bf16 (8 bits) has fp32's range: m is taken
+// from a row's first columns and moves only when weights pass 2^60.  fp16 (11
+// bits) is held below 2^15 with m's weight at 2^3, which keeps 11 bits down to
+// 2^-17 of that and some down to 2^-27.  When m moves, O is rescaled in tensor
+// memory by the row's own thread.
 //
 // Roles (16 warps): warps 0-3 and 4-7 are the softmax of tile 0 and 1, a
 // thread a row; warps 8-11 bring V, converting it in registers; warp 12 issues
@@ -60,13 +60,24 @@ constexpr int kQBytes = kTileRows * kPitch;
 constexpr int kKBytes = kTile * kPitch;
 constexpr int kVHalf = kTile * 128;      // 64 channels of bf16
 constexpr int kVBytes = 2 * kVHalf;
-constexpr float kLazy = 12.0f;
-constexpr float kWeight = 8.0f;          // weights are this times 2^(s - m) vs
+constexpr int kPart = 32;                // columns a softmax thread has in registers
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kWaitTries = 1 << 20;
 __host__ __device__ constexpr UnitShape unit_shape() {
   return UnitShape{kBlockRows, kTile, kRowLimit + 1, int64_t{1} << 40};
 }
+
+// P and V are of the queries' type.  An entry of P is `unit` 2^(s - m) vs, and
+// the sum of kPart of them may reach `limit` before m has to move.
+template <typename W> struct Weight;
+template <> struct Weight<__nv_bfloat16> {
+  static constexpr float unit = 1.0f, limit = 1.152921504606846976e18f;  // 2^60
+  static constexpr int type = 1;
+};
+template <> struct Weight<__half> {
+  static constexpr float unit = 8.0f, limit = 32768.0f;
+  static constexpr int type = 0;
+};
 
 template <int NS>
 struct Plan {
@@ -124,6 +135,14 @@ __device__ __forceinline__ void wait(Bars* B, uint64_t* bar, uint32_t parity) {
   __syncwarp();
 }
 
+// As wait(), for up to three barriers at once: lane 0 looks at the first, lane
+// 1 at the second, the others at the third.
+__device__ __forceinline__ void wait3(Bars* B, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                      uint64_t* c, uint32_t pc) {
+  const int lane = threadIdx.x & 31;
+  wait(B, lane == 0 ? a : lane == 1 ? b : c, lane == 0 ? pa : lane == 1 ? pb : pc);
+}
+
 // One arrival a warp (32 arrivals on one word would take their turns).
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   __syncwarp();
@@ -136,11 +155,6 @@ __device__ __forceinline__ void tile_sync(int t) {
   asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ float lg2(float x) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -189,7 +203,7 @@ __host__ __device__ constexpr int64_t partial_floats(int head_dim) {
 // Three warps: finds the places of a unit's positions in the cache, two units
 // ahead (unit J's table entries are read at J - 2, its scales at J - 1), and
 // copies K.  A thread has positions tid and tid + 96 (below 128).
-template <int NS>
+template <typename T, int NS>
 __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t* smem, Bars* B) {
   using L = Plan<NS>;
   const int tid = threadIdx.x - 13 * 32;
@@ -296,7 +310,7 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
       if (i == 0 || second) {
         const int tok = tid + i * kPlaceThreads;
         float* at = s_sc + slot * 3 * kTile + tok;
-        const float lv = lg2(fmaxf(v0[i], 5.42101086e-20f)), vw = v0[i] * kWeight;  // 2^-64
+        const float lv = lg2(fmaxf(v0[i], 5.42101086e-20f)), vw = v0[i] * Weight<T>::unit;  // 2^-64
         at[0] = k0[i];
         at[kTile] = lv;
         at[2 * kTile] = vw;
@@ -335,12 +349,25 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
   arrive(&B->k_full[kr.slot == 0 ? L::kK - 1 : kr.slot - 1]);
 }
 
-// 16 codes to 16 fp16; exact.
-__device__ __forceinline__ void to_f16(const uint4& c, uint4& lo, uint4& hi) {
-  lo = make_uint4(e4m3x2_to_f16x2(c.x), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y),
-                  e4m3x2_to_f16x2(c.y >> 16));
-  hi = make_uint4(e4m3x2_to_f16x2(c.z), e4m3x2_to_f16x2(c.z >> 16), e4m3x2_to_f16x2(c.w),
-                  e4m3x2_to_f16x2(c.w >> 16));
+// 16 codes to 16 values of 16 bits; exact.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& c, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[2 * k] = e4m3x2_to_f16x2(w[k]);
+    o[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+  }
+  if (Weight<T>::type == 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 x = Pair<__half>::unpack(o[k]);
+      o[k] = Pair<T>::pack(x.x, x.y);
+    }
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // Zeroes the NaN codes of a word; true if there were any.
@@ -350,9 +377,9 @@ __device__ __forceinline__ bool drop_nans(uint32_t& w) {
   return hit != 0u;
 }
 
-// Four warps: V, a unit ahead in registers, made fp16 on its way to shared
-// memory.  A thread has 16 channels (one 16-byte chunk) of 8 positions.
-template <int NS>
+// Four warps: V, a unit ahead in registers, made 16 bits wide on its way to
+// shared memory.  A thread has 16 channels (one 16-byte chunk) of 8 positions.
+template <typename T, int NS>
 __device__ __noinline__ void value_role(const AttendParams& P, int units, uint8_t* smem, Bars* B) {
   using L = Plan<NS>;
   const int tid = threadIdx.x & 127;
@@ -398,7 +425,7 @@ __device__ __noinline__ void value_role(const AttendParams& P, int units, uint8_
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         uint4 lo, hi;
-        to_f16(raw[i], lo, hi);
+        widen<T>(raw[i], lo, hi);
         // (16 positions on, the swizzle is the same.)
         *reinterpret_cast<uint4*>(dst + first + i * 16 * 128) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(dst + other + i * 16 * 128) = swap ? lo : hi;
@@ -425,13 +452,13 @@ __device__ __noinline__ void value_role(const AttendParams& P, int units, uint8_
 
 // One whole warp, so that its operands stay in uniform registers; one elected
 // lane issues.
-template <int NS>
+template <typename T, int NS>
 __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* smem, Bars* B) {
   using L = Plan<NS>;
   const uint32_t tmem = __shfl_sync(kFull, B->tmem, 0);
   const int ksteps = (P.c.head_dim + 31) >> 5;
   const uint32_t qk_instr = tc::instruction(0, kTile, false);
-  const uint32_t pv_instr = tc::instruction(0, P.c.head_dim, true);
+  const uint32_t pv_instr = tc::instruction(Weight<T>::type, P.c.head_dim, true);
   constexpr uint32_t kHi = tc::operand_hi(1024);
   const uint32_t q0 = tc::operand_lo(smem_addr(smem + L::q), 16);
   const uint32_t k0 = tc::operand_lo(smem_addr(smem + L::k), 16);
@@ -474,11 +501,11 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
       const uint32_t vd = v0 + vr.slot * (kVBytes / 16);
       const bool more = j + 1 < n;
       for (int t = 0; t < tiles; ++t) {
-        if (t == 0) {
-          wait(B, &B->v_full[vr.slot], vr.phase);
-          if (more) wait(B, &B->k_full[kr.slot], kr.phase);
-        }
-        wait(B, &B->p_full[t], (p_phase >> t) & 1u);
+        uint64_t* p = &B->p_full[t];
+        const uint32_t phase = (p_phase >> t) & 1u;
+        // (V, and K of the next unit where there is one.)
+        wait3(B, p, phase, &B->v_full[vr.slot], vr.phase, more ? &B->k_full[kr.slot] : p,
+              more ? kr.phase : phase);
         p_phase ^= 1u << t;
         tc::fence_after();
         if (tc::elect()) {
@@ -504,127 +531,135 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
 
 // ------------------------------------------------------------------ softmax
 
-// Moves a row's reference by a factor f of its O.  (A function of its own, as
-// are the rarer forms of the softmax below: the loop that runs for every unit
-// stays small enough for the instruction caches.)
-__device__ __noinline__ void rescale(uint32_t o_tmem, int d, float f) {
+// Multiplies what a row has summed by f, when its reference moves: O (not yet
+// there in a block's first unit) and the `done` columns of P that this unit has
+// written.  (A function of its own, as are the rarer forms of the softmax
+// below: the loop that runs for every unit stays small enough for the
+// instruction caches.)
+template <typename W>
+__device__ __noinline__ void rescale(uint32_t o_tmem, int d, uint32_t p_tmem, int done, float f) {
 #pragma unroll 1
   for (int k = 0; k < d; k += 32) {
     uint32_t o[32];
     tc::ld32(o_tmem + k, o);  // (past d: columns that nothing reads)
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-    tc::st16(o_tmem + k, o);
-    tc::st16(o_tmem + k + 16, o + 16);
+    tc::st32(o_tmem + k, o);
+  }
+#pragma unroll 1
+  for (int k = 0; k < done; k += 16) {
+    uint32_t p[16];
+    tc::ld16(p_tmem + k, p);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = Pair<W>::unpack(p[i]);
+      p[i] = Pair<W>::pack(x.x * f, x.y * f);
+    }
+    tc::st16(p_tmem + k, p);
   }
 }
 
-// One row's softmax of one unit: reads S, moves the running maximum m (and O
-// with it), adds to l, leaves P in S's place.  MASK: columns outside [from, to]
-// are not seen.  GROUPS: scales are the same over 16 columns.
-//
-// S is read twice, 32 columns at a time: more would not fit the registers.
+// The largest s + log2 vs of kPart columns of a row.
 template <bool MASK, bool GROUPS>
+__device__ __noinline__ float highest(uint32_t s_tmem, const float* sc, const float4* gr, int from,
+                                      int to, float factor) {
+  uint32_t x[kPart];
+  tc::ld32(s_tmem, x);
+  float most = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kPart; ++k) {
+    const float ks = GROUPS ? gr[k / 16].x : sc[k], lv = GROUPS ? gr[k / 16].y : sc[kTile + k];
+    const float t = fmaf(__uint_as_float(x[k]), ks * factor, lv);
+    if (!MASK || (k >= from && k <= to)) most = fmaxf(most, t);
+  }
+  return most;
+}
+
+// One row's softmax of one unit: reads S, adds to l, leaves P in S's place.
+// MASK: columns outside [from, to] are not seen.  GROUPS: scales are the same
+// over 16 columns.  W: P's type.
+//
+// S goes through the registers kPart columns at a time (all 128 would not fit).
+// The reference m is not the running maximum but one from the row's first
+// columns, for as long as the weights under it stay below W's limit; their sum
+// shows that, so no maximum is taken.  Where it is passed, m and what was
+// summed under it move, and the columns are done again.
+template <bool MASK, bool GROUPS, typename W>
 __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
                                                const float4* gr, int from, int to, float factor,
                                                int o_cols, float m, float l) {
-  auto mask = [&](uint32_t (&x)[32], int q) {
-    if (MASK) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (32 * q + k < from || 32 * q + k > to) x[k] = 0xff800000u;
-    }
-  };
-  // ---- the row's largest s + log2 vs
-  float most = -INFINITY;
 #pragma unroll 1
-  for (int q = 0; q < kTile / 32; ++q) {
-    uint32_t x[32];
-    tc::ld32(s_tmem + 32 * q, x);
-    mask(x, q);
-    if (GROUPS) {
+  for (int q = 0; q < kTile / kPart; ++q) {
+    uint32_t p[kPart / 2];
+    uint64_t sum = 0ull;  // of the weights
+    bool moved = false;
+    for (;;) {
+      uint32_t x[kPart];
+      tc::ld32(s_tmem + kPart * q, x);
+      if (MASK) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float4 scale = gr[2 * q + g];
-        float a = __uint_as_float(x[16 * g]), b = __uint_as_float(x[16 * g + 1]);
+        for (int k = 0; k < kPart; ++k)
+          if (k < from || k > to) x[k] = 0xff800000u;
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      const uint64_t r2 = pack2(-ref, -ref);
+      sum = 0ull;
+      uint64_t held = 0ull;  // what P's entries sum to
 #pragma unroll
-        for (int k = 2; k < 16; k += 4) {
-          a = max3(a, __uint_as_float(x[16 * g + k]), __uint_as_float(x[16 * g + k + 1]));
-          if (k + 3 < 16)
-            b = max3(b, __uint_as_float(x[16 * g + k + 2]), __uint_as_float(x[16 * g + k + 3]));
+      for (int g = 0; g < kPart / 16; ++g) {
+        float4 scale;
+        if (GROUPS) scale = gr[g];
+        const float fg = scale.x * factor;
+        const uint64_t fg2 = pack2(fg, fg), vg2 = pack2(scale.z, scale.z);
+        uint64_t gsum = 0ull;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          uint64_t f = fg2, v = vg2;
+          const int col = 16 * g + i;
+          if (!GROUPS) {
+            const float2 ks = *reinterpret_cast<const float2*>(sc + col);
+            const float2 vs = *reinterpret_cast<const float2*>(sc + 2 * kTile + col);
+            f = mul2(pack2(ks.x, ks.y), pack2(factor, factor));
+            v = pack2(vs.x, vs.y);
+          }
+          const float2 a = unpack2(
+              fma2(pack2(__uint_as_float(x[col]), __uint_as_float(x[col + 1])), f, r2));
+          const uint64_t w = pack2(ex2(a.x), ex2(a.y));
+          gsum = i == 0 ? w : add2(gsum, w);
+          const uint64_t pw = mul2(w, v);
+          if (!GROUPS) held = add2(held, pw);
+          const float2 pa = unpack2(pw);
+          p[col / 2] = Pair<W>::pack(pa.x, pa.y);
         }
-        most = fmaxf(most, fmaf(fmaxf(a, b), scale.x * factor, scale.y));
+        sum = g == 0 ? gsum : add2(sum, gsum);
+        if (GROUPS) held = fma2(gsum, vg2, held);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * q + k);
-        const float4 lv = *reinterpret_cast<const float4*>(sc + kTile + 32 * q + k);
-        const float a = fmaf(__uint_as_float(x[k]), ks.x * factor, lv.x);
-        const float b = fmaf(__uint_as_float(x[k + 1]), ks.y * factor, lv.y);
-        const float c = fmaf(__uint_as_float(x[k + 2]), ks.z * factor, lv.z);
-        const float e = fmaf(__uint_as_float(x[k + 3]), ks.w * factor, lv.w);
-        most = max3(most, max3(a, b, c), e);
-      }
+      const float2 h = unpack2(held);
+      const bool past = !(h.x + h.y <= Weight<W>::limit) || m == -INFINITY;
+      if (moved || !__any_sync(kFull, past)) break;
+      const float most = highest<MASK, GROUPS>(s_tmem + kPart * q, sc, gr, from, to, factor);
+      const float now = past ? fmaxf(m, most) : m;
+      const float f = m == -INFINITY ? 0.0f : ex2(m - now);
+      m = now;
+      l *= f;
+      rescale<W>(o_tmem, o_cols, s_tmem, kPart / 2 * q, f);
+      moved = true;
     }
+    tc::st16(s_tmem + kPart / 2 * q, p);  // over columns that have been read
+    const float2 s = unpack2(sum);
+    l += s.x + s.y;
+    gr += kPart / 16;
+    sc += kPart;
+    from -= kPart, to -= kPart;
   }
-  const bool rise = most > m + kLazy;
-  if (__any_sync(kFull, rise)) {
-    const float now = rise ? most : m;
-    const float f = m == -INFINITY ? 0.0f : ex2(m - now);
-    m = now;
-    l *= f;
-    if (o_cols > 0) rescale(o_tmem, o_cols, f);
-  }
-  // ---- weights
-  const float ref = m == -INFINITY ? 0.0f : m;
-  const uint64_t r2 = pack2(-ref, -ref);
-  uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll 1
-  for (int q = 0; q < kTile / 32; ++q) {
-    uint32_t x[32], p[16];
-    tc::ld32(s_tmem + 32 * q, x);
-    mask(x, q);
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      float4 scale;
-      if (GROUPS) scale = gr[2 * q + g];
-      const float fg = scale.x * factor;
-      const uint64_t fg2 = pack2(fg, fg), vg2 = pack2(scale.z, scale.z);
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        uint64_t f0 = fg2, f1 = fg2, v0 = vg2, v1 = vg2;
-        const int col = 16 * g + i;
-        if (!GROUPS) {
-          const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * q + col);
-          const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + 32 * q + col);
-          const uint64_t ff = pack2(factor, factor);
-          f0 = mul2(pack2(ks.x, ks.y), ff), f1 = mul2(pack2(ks.z, ks.w), ff);
-          v0 = pack2(vs.x, vs.y), v1 = pack2(vs.z, vs.w);
-        }
-        const float2 a = unpack2(
-            fma2(pack2(__uint_as_float(x[col]), __uint_as_float(x[col + 1])), f0, r2));
-        const float2 b = unpack2(
-            fma2(pack2(__uint_as_float(x[col + 2]), __uint_as_float(x[col + 3])), f1, r2));
-        const uint64_t wa = pack2(ex2(a.x), ex2(a.y)), wb = pack2(ex2(b.x), ex2(b.y));
-        sum[0] = add2(sum[0], wa);
-        sum[1] = add2(sum[1], wb);
-        const float2 pa = unpack2(mul2(wa, v0)), pb = unpack2(mul2(wb, v1));
-        p[col / 2] = Pair<__half>::pack(pa.x, pa.y);
-        p[col / 2 + 1] = Pair<__half>::pack(pb.x, pb.y);
-      }
-    }
-    tc::st16(s_tmem + 16 * q, p);  // over columns that have been read
-  }
-  const float2 s = unpack2(add2(sum[0], sum[1]));
-  return make_float2(m, l + (s.x + s.y));
+  return make_float2(m, l);
 }
 
-template <bool GROUPS>
+template <bool GROUPS, typename W>
 __device__ __noinline__ float2 softmax_masked(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
                                               const float4* gr, int from, int to, float factor,
                                               int o_cols, float m, float l) {
-  return softmax_unit<true, GROUPS>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
+  return softmax_unit<true, GROUPS, W>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
 }
 
 // What a block's units need of one softmax thread.
@@ -638,6 +673,7 @@ struct RowState {
 //   from, to: columns of the first unit that the row sees, going down by kTile
 //   a unit; all_from, all_to: those that every row of the tile sees;
 //   tile: bit 0 the tile, bit 1 scales by groups may be used.
+template <typename W>
 __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float* s_sc,
                                                const float4* s_gr, uint32_t s_tmem, uint32_t o_tmem,
                                                float factor, int d, int n, int from, int to,
@@ -655,11 +691,11 @@ __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float*
     const bool groups = (tile & 2) != 0 && (mixed[0] | mixed[1] | mixed[2]) == 0;
     float2 ml;
     if (groups && all_from <= 0 && all_to >= kTile - 1) {
-      ml = softmax_unit<false, true>(s_tmem, o_tmem, nullptr, gr, 0, 0, factor, cols, r.m, r.l);
+      ml = softmax_unit<false, true, W>(s_tmem, o_tmem, s_sc, gr, 0, 0, factor, cols, r.m, r.l);
     } else {
       const float* sc = s_sc + slot * 3 * kTile;
-      ml = groups ? softmax_masked<true>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
-                  : softmax_masked<false>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
+      ml = groups ? softmax_masked<true, W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
+                  : softmax_masked<false, W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
     }
     r.m = ml.x;
     r.l = ml.y;
@@ -777,7 +813,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       const int base = c.k.start + t_begin * kTile;
       st.m = -INFINITY;
       st.l = 0.0f;
-      st = softmax_units(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
+      st = softmax_units<T>(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
                          all_lo - base, all_hi - base, tile);
     }
     // ---- the block's end: O is complete
@@ -814,7 +850,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         P.lse[j_row * P.q_heads + head] = ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     };
     if (whole) {
-      const float inv = l != 0.0f ? (1.0f / kWeight) / l : 0.0f;
+      const float inv = l != 0.0f ? (1.0f / Weight<T>::unit) / l : 0.0f;
 #pragma unroll 1
       for (int k = 0; k < d; k += 16) {
         uint32_t r[16];
@@ -879,7 +915,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
           const float2 s = stat_of(cta, tid);
           ll += s.y * ex2(s.x - ref);
         }
-        const float inv = ll != 0.0f ? (1.0f / kWeight) / ll : 0.0f;
+        const float inv = ll != 0.0f ? (1.0f / Weight<T>::unit) / ll : 0.0f;
 #pragma unroll 1
         for (int k = 0; k < d; k += 16) {
           float o[16];
@@ -954,11 +990,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
   if (warp < 8) {
     softmax_role<T, NS>(P, c, range, smem, B, warp >> 2);
   } else if (warp < 12) {
-    value_role<NS>(P, static_cast<int>(c.left), smem, B);
+    value_role<T, NS>(P, static_cast<int>(c.left), smem, B);
   } else if (warp == 12) {
-    mma_role<NS>(P, c, smem, B);
+    mma_role<T, NS>(P, c, smem, B);
   } else {
-    place_role<NS>(P, c, smem, B);
+    place_role<T, NS>(P, c, smem, B);
   }
   // Every product has been waited for (by the last block's softmax).
   __syncwarp();

@@ -337,3 +337,20 @@ def test_calls_of_different_shapes_share_a_workspace():
     for _ in range(2):
         for (p, c, q), want in zip(problems, fresh):
             assert torch.equal(call(p, c, q, workspace=shared)[0], want)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("new", [1, 3, 130])
+@pytest.mark.parametrize("rising", [True, False])
+def test_scores_that_rise_or_fall_along_the_keys(dt, new, rising):
+    # Keys grow (or shrink) from page to page, so that a reference taken from the first
+    # ones is far from the last ones, by more than the largest power of two of fp32.
+    p = ref.page_problem([400], [new], 16, 1, 64, 70)
+    q = queries(new, 1, 64, dt, 18, gain=3.0)
+    pages = (p["page_table"][int(p["table_idx"][0]), ::16] // 16).long()
+    e = torch.linspace(-8.0, 2.0, len(pages)).round()
+    p["k_scale"][pages, 0] = torch.exp2(e if rising else e.flip(0))
+    p["v_scale"][pages, 0] = torch.exp2((-e if rising else e) * 3.0)
+    out, lse, status = call(p, make_cache(p), q)
+    assert status == 0
+    check(p, q, out, lse)
