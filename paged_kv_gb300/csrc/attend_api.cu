@@ -105,7 +105,7 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   P.counters = counters;
   cudaError_t e = launch_attend_rows(P, row_block(max_q_len, group), row_ctas(sms), st);
   if (e == cudaSuccess && has_tiles(max_q_len, group)) {
-    P.counters = counters + row_ctas(sms);
+    P.counters = counters + row_counters(sms);
     e = launch_attend_tiles(P, tile_ctas(sms), st);
   }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");

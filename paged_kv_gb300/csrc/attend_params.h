@@ -64,11 +64,12 @@ inline bool has_tiles(int max_q_len, int group) {
 // the device alone, so that calls of any shape can follow one another on it.
 // The partial results come after; the kernels run one after the other and use
 // the same bytes for theirs.
-constexpr int kRowCtasPerSm = 2;
+constexpr int kRowCtasPerSm = 3, kRowWarps = 4;
 inline int row_ctas(int num_sms) { return num_sms * kRowCtasPerSm; }
+inline int row_counters(int num_sms) { return 3 * kRowWarps * row_ctas(num_sms); }
 inline int tile_ctas(int num_sms) { return num_sms; }
 inline size_t counter_bytes(int num_sms) {
-  return (static_cast<size_t>(row_ctas(num_sms) + 2 * tile_ctas(num_sms)) * 4 + 255) / 256 * 256;
+  return (static_cast<size_t>(row_counters(num_sms) + 2 * tile_ctas(num_sms)) * 4 + 255) / 256 * 256;
 }
 
 // Rows (query token, query head of one cache head) in a block of the row

@@ -2,25 +2,26 @@
 // (one token a request), verification of a few draft tokens.
 //
 // A row is one (query token, query head); the rows of one cache head share its
-// keys and values.  A work unit is a tile of kTile positions for one block of
-// up to 8 * NT rows of one (request, cache head).  All units of the call, in
-// batch order, are cut into equal contiguous ranges, one per CTA, so ragged
-// lengths balance and one long request fills the machine.  A CTA that holds
-// only part of a block's units leaves its partial (m, l, O) in the workspace;
-// the last of the block's CTAs to finish joins the partials in CTA order.
+// keys and values.  A work unit is kStep positions for one block of up to 8 * NT
+// rows of one (request, cache head).  All units of the call, in batch order,
+// are cut into equal contiguous ranges, one per warp, so ragged lengths balance
+// and one long request fills the machine.  A warp that holds only part of a
+// block leaves its partial (m, l, O) in the workspace; partials are joined in
+// warp order, first within groups of kGroup warps, then over the groups, each
+// time by the last to arrive, so that no join is long and every sum has one
+// order.  Warps share nothing: there is no barrier after the start.
 //
-// Inside a CTA each warp streams its own 16-position steps through its own
-// ring of shared memory (cp.async) and keeps its own running softmax; the
-// warps meet once at the end of a block.  Per step, with keys and values as
-// the A operand so that the few rows are the narrow side of the product:
-//   S^T[16 x 8] = K[16 x D] Q^T,   O^T[D x 8] += V^T[D x 16] P^T
+// A warp streams its units through its own ring of shared memory (cp.async).
+// Per unit, with keys and values as the A operand so that the few rows are the
+// narrow side of the product:
+//   S^T[32 x 8] = K[32 x D] Q^T,   O^T[D x 8] += V^T[D x 32] P^T
 // on mma.m16n8k16 with fp16 inputs: e4m3 codes are exact in fp16, and a query
 // is scaled to at most 2 by a power of two, so the products are exact.  Scores
 // take the page's key scale in fp32.  Weights carry the page's value scale:
 // with m the running maximum of s + log2(vs), p = 2^(s - m) vs <= 2^8 goes to
 // fp16 (11 bits), and l sums 2^(s - m) in fp32, so neither over- nor
 // underflows for any scales.  m moves only when it would rise by more than 8:
-// sums stay far below fp16's and fp32's limits and most steps rescale nothing.
+// sums stay far below fp16's and fp32's limits and most units rescale nothing.
 //
 // Bound: bytes.  Each cached byte is read once (2 D per position and head).
 
@@ -41,27 +42,24 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStep = 16;                // positions a warp takes at a time
-constexpr int kTile = kWarps * kStep;    // positions of a work unit
-constexpr int kStages = 4;               // ring slots of a warp
+constexpr int kWarps = kRowWarps;
+constexpr int kStep = 32;                // positions a warp takes at a time: one a lane
+constexpr int kStages = 2;               // ring slots of a warp
+constexpr int kGroup = 16;               // warps whose partials are joined first
+static_assert(kStep == 32, "a lane looks up one position");
 constexpr float kLazy = 8.0f;            // log2 of how far sums may outgrow their reference
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int DP>
 struct Layout {
-  static constexpr int kPitch = DP + 8;                    // floats a row of the joining buffer
   static constexpr int kSlot = 2 * kStep * DP;             // K then V codes
   static constexpr int kScales = 2 * kStep * 4;            // key then value scales
-  static constexpr int kRing = kWarps * kStages * (kSlot + kScales);
+  static constexpr int kRing = kStages * (kSlot + kScales);
+  static constexpr int kBytes = kWarps * kRing;
+  static_assert(kBytes >= kWarps * 32 * 16 + 16, "room for find_range");
 };
 
-template <int DP, int NT>
-constexpr int smem_bytes() {
-  return Layout<DP>::kRing + kWarps * 8 * NT * Layout<DP>::kPitch * 4 + kWarps * 8 * NT * 8 + 64;
-}
-
-// Floats of one partial result: O [rows, DP], then m and l [rows].
+// Floats of one partial result: O [rows, DP], then (m, l) [rows].
 __host__ __device__ constexpr int partial_floats(int rows, int dp) { return rows * dp + 2 * rows; }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
@@ -119,28 +117,99 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
 }
 
+// Joins the partials of slots slot_of(0) .. slot_of(n - 1), in this order, and
+// hands each row's m, l and 4 channels of O to put(row, d, m, l, o).  One warp;
+// a lane has 4 channels of kJoin rows, and 4 partials of them on their way:
+// the join is at the end of everything and waits for memory alone.
+template <int DP, int ROWS, typename Slot, typename Put>
+__device__ __forceinline__ void join(const AttendParams& P, int rows, int n, Slot&& slot_of, Put&& put) {
+  constexpr int kFloats = partial_floats(ROWS, DP), kJoin = 4;
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const bool live = d < P.c.head_dim;
+  for (int r0 = 0; r0 < rows; r0 += kJoin) {
+    float m[kJoin], l[kJoin];
+    float4 o[kJoin];
+#pragma unroll
+    for (int r = 0; r < kJoin; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+      o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      // Lane i has partial c0 + i's statistics.
+      const int cnt = min(32, n - c0);
+      float f[kJoin], ls[kJoin];
+#pragma unroll
+      for (int r = 0; r < kJoin; ++r) {
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < cnt && r0 + r < rows)
+          ml = __ldcg(reinterpret_cast<const float2*>(P.partials + slot_of(c0 + lane) * kFloats +
+                                                      ROWS * DP) + r0 + r);
+        f[r] = ml.x;
+        ls[r] = ml.y;
+      }
+#pragma unroll
+      for (int r = 0; r < kJoin; ++r) {
+        float top = f[r];
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+        const float now = fmaxf(m[r], top);
+        const float ref = now == -INFINITY ? 0.0f : now;
+        const float keep = ex2(m[r] - ref);
+        f[r] = ex2(f[r] - ref);
+        m[r] = now;
+        l[r] *= keep;
+        o[r].x *= keep, o[r].y *= keep, o[r].z *= keep, o[r].w *= keep;
+      }
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float* p = P.partials + slot_of(c0 + i) * kFloats + r0 * DP + d;
+        float4 x[kJoin];
+#pragma unroll
+        for (int r = 0; r < kJoin; ++r) {
+          x[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (live && r0 + r < rows) x[r] = __ldcg(reinterpret_cast<const float4*>(p + r * DP));
+        }
+#pragma unroll
+        for (int r = 0; r < kJoin; ++r) {
+          const float fi = __shfl_sync(kFull, f[r], i), li = __shfl_sync(kFull, ls[r], i);
+          if (li != 0.0f) {  // otherwise that part saw nothing
+            l[r] = fmaf(li, fi, l[r]);
+            o[r].x = fmaf(x[r].x, fi, o[r].x);
+            o[r].y = fmaf(x[r].y, fi, o[r].y);
+            o[r].z = fmaf(x[r].z, fi, o[r].z);
+            o[r].w = fmaf(x[r].w, fi, o[r].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoin; ++r)
+      if (live && r0 + r < rows) put(r0 + r, d, m[r], l[r], o[r]);
+  }
+}
+
 template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel(const AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel(
+    const __grid_constant__ AttendParams P) {
   using L = Layout<DP>;
   constexpr int kRows = 8 * NT;
   constexpr int kChunks = DP / 16;
-  constexpr UnitShape kShape{kRows, kTile, 1, kRowLimit};
+  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit};
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_o = reinterpret_cast<float*>(smem + L::kRing);
-  float2* s_ml = reinterpret_cast<float2*>(s_o + kWarps * kRows * L::kPitch);
-  int* s_last = reinterpret_cast<int*>(s_ml + kWarps * kRows);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row_lane = lane >> 2, col_lane = lane & 3;
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
 
   Cursor ld;  // where this warp loads
-  const Range range = find_range<kWarps * 32>(P, kShape, smem, &ld);
+  const Range range = find_range<kWarps * 32, kWarps>(P, kShape, smem, &ld);
   if (ld.left == 0) return;
   Cursor cu = ld;  // where it computes
 
   // Ring: columns past head_dim stay zero throughout.
-  const uint32_t ring = smem_addr(smem) + warp * kStages * (L::kSlot + L::kScales);
+  const uint32_t ring = smem_addr(smem) + warp * L::kRing;
   if (P.c.head_dim < DP) {
-    for (int i = lane; i < kStages * (L::kSlot + L::kScales) / 16; i += 32)
+    for (int i = lane; i < L::kRing / 16; i += 32)
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * 16), "r"(0) : "memory");
     __syncwarp();
   }
@@ -153,15 +222,14 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   const int chunks = P.c.head_dim >> 4;
   int issued = 0;
 
-  // Copies the next step of this warp's share, or commits an empty group.
+  // Copies the next unit, or commits an empty group.
   auto issue = [&]() {
-    while (ld.left > 0) {
-      const int base = ld.k.start + ld.tile * kTile + warp * kStep;
-      const bool some = base < ld.k.end;
-      if (some) {
+    if (ld.left > 0) {
+      const int base = ld.k.start + ld.tile * kStep;
+      {
         const uint32_t slot = ring + (issued % kStages) * (L::kSlot + L::kScales);
         ++issued;
-        const int tok = base + (lane & 15);
+        const int tok = base + lane;
         bool valid = tok >= ld.k.lo && tok < ld.k.end;
         int loc = 0;
         if (valid) loc = P.page_table[ld.r.table_row * P.pt_cols + tok];
@@ -173,6 +241,9 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         const int page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(loc)));
         const int64_t at = page * P.c.page_stride + (loc - page * ps) * P.c.token_stride +
                            ld.head * P.c.head_stride;
+        const int64_t sc = static_cast<int64_t>(page) * P.c.kv_heads + ld.head;
+        cp_async4_zfill(slot + L::kSlot + lane * 4, P.c.k_scale + sc, valid);
+        cp_async4_zfill(slot + L::kSlot + kStep * 4 + lane * 4, P.c.v_scale + sc, valid);
         const unsigned ok = __ballot_sync(kFull, valid);
         constexpr int kPer = 32 / kChunks;  // positions a round of the warp covers
         const int ch = lane % kChunks;
@@ -187,13 +258,9 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
             cp_async16_zfill(dst + kStep * DP, static_cast<const uint8_t*>(P.c.v) + off + ch * 16, v);
           }
         }
-        const float* sc = lane < 16 ? P.c.k_scale : P.c.v_scale;
-        cp_async4_zfill(slot + L::kSlot + lane * 4,
-                        sc + static_cast<int64_t>(page) * P.c.kv_heads + ld.head, valid);
       }
       --ld.left;
       if (++ld.tile >= ld.k.tiles && ld.left > 0) next_block(P, ld, kShape);
-      if (some) break;
     }
     cp_async_commit();
   };
@@ -258,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         const int r = nt * 8 + 2 * col_lane + c;
         cf[nt][c] = P.scale_log2 / __shfl_sync(kFull, unit, (2 * col_lane + c) * 4);
         const int p = cu.r.cached + (cu.k.row0 + r) / P.group;
-        hi[nt][c] = r < cu.k.rows ? p : -1;
+        hi[nt][c] = r < cu.k.rows ? min(p, cu.k.end - 1) : -1;
         lo[nt][c] = cu.r.begin;
         if (P.window > 0) lo[nt][c] = max(lo[nt][c], p - P.window + 1);
         if (r < cu.k.rows) {
@@ -277,39 +344,47 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     all_lo = __reduce_max_sync(kFull, all_lo);
 
     for (int tile = t_begin; tile < t_end; ++tile) {
-      const int base = cu.k.start + tile * kTile + warp * kStep;
-      if (base >= cu.k.end) continue;
+      const int base = cu.k.start + tile * kStep;
       cp_async_wait<kStages - 2>();
       __syncwarp();
       const uint32_t slot = ring + (used % kStages) * (L::kSlot + L::kScales);
       ++used;
-      // ---- S^T = K Q^T
-      float s[NT][4];
+      // ---- S^T = K Q^T, two tiles of 16 positions
+      constexpr int kM = kStep / 16;
+      float s[kM][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
 #pragma unroll
       for (int w = 0; w < DP / 64; ++w) {
         const int ch = col_lane * (DP / 64) + w;
-        const uint4 a = lds128(slot + chunk_at(row_lane, ch));
-        const uint4 b = lds128(slot + chunk_at(row_lane + 8, ch));
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = e4m3x2_to_f16x2(aw[j]), a2 = e4m3x2_to_f16x2(aw[j] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(bw[j]), a3 = e4m3x2_to_f16x2(bw[j] >> 16);
+        for (int mt = 0; mt < kM; ++mt) {
+          const uint4 a = lds128(slot + chunk_at(16 * mt + row_lane, ch));
+          const uint4 b = lds128(slot + chunk_at(16 * mt + row_lane + 8, ch));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(s[nt], a0, a1, a2, a3, qf[nt][8 * w + 2 * j], qf[nt][8 * w + 2 * j + 1]);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = e4m3x2_to_f16x2(aw[j]), a2 = e4m3x2_to_f16x2(aw[j] >> 16);
+            const uint32_t a1 = e4m3x2_to_f16x2(bw[j]), a3 = e4m3x2_to_f16x2(bw[j] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][8 * w + 2 * j], qf[nt][8 * w + 2 * j + 1]);
+          }
         }
       }
-      // ---- softmax
+      // ---- softmax.  Position i of this thread: base + 8 i + row_lane.
       const uint32_t sc = slot + L::kSlot + row_lane * 4;
-      const float ks0 = lds32(sc), ks1 = lds32(sc + 32);
-      const float vs0 = lds32(sc + 64), vs1 = lds32(sc + 96);
-      const float lv0 = lg2(fmaxf(vs0, 5.42101086e-20f)), lv1 = lg2(fmaxf(vs1, 5.42101086e-20f));
-      const int p0 = base + row_lane, p1 = p0 + 8;
+      float ks[2 * kM], vs[2 * kM], lv[2 * kM];
+#pragma unroll
+      for (int i = 0; i < 2 * kM; ++i) {
+        ks[i] = lds32(sc + 32 * i);
+        vs[i] = lds32(sc + kStep * 4 + 32 * i);
+        lv[i] = lg2(fmaxf(vs[i], 5.42101086e-20f));
+      }
       const bool partial = base < all_lo || base + kStep - 1 > all_hi;  // uniform
       float top[NT][2];
       bool rise = false;
@@ -317,13 +392,17 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          s[nt][c] *= ks0 * cf[nt][c];
-          s[nt][2 + c] *= ks1 * cf[nt][c];
-          if (partial) {
-            if (p0 < lo[nt][c] || p0 > hi[nt][c]) s[nt][c] = -INFINITY;
-            if (p1 < lo[nt][c] || p1 > hi[nt][c]) s[nt][2 + c] = -INFINITY;
+          float t = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 2 * kM; ++i) {
+            float& x = s[i >> 1][nt][2 * (i & 1) + c];
+            x *= ks[i] * cf[nt][c];
+            if (partial) {
+              const int p = base + 8 * i + row_lane;
+              if (p < lo[nt][c] || p > hi[nt][c]) x = -INFINITY;
+            }
+            t = fmaxf(t, x + lv[i]);
           }
-          float t = fmaxf(s[nt][c] + lv0, s[nt][2 + c] + lv1);
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
@@ -348,89 +427,93 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           }
         }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[kM][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+        const float r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float ref = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
-          w[c] = ex2(s[nt][c] - ref);
-          w[2 + c] = ex2(s[nt][2 + c] - ref);
-          l[nt][c] += w[c] + w[2 + c];
+        for (int i = 0; i < 2 * kM; ++i) {
+          const float a = ex2(s[i >> 1][nt][2 * (i & 1)] - r0);
+          const float b = ex2(s[i >> 1][nt][2 * (i & 1) + 1] - r1);
+          l[nt][0] += a;
+          l[nt][1] += b;
+          pf[i >> 1][nt][i & 1] = transpose8x8(Pair<__half>::pack(a * vs[i], b * vs[i]));
         }
-        pf[nt][0] = transpose8x8(Pair<__half>::pack(w[0] * vs0, w[1] * vs0));
-        pf[nt][1] = transpose8x8(Pair<__half>::pack(w[2] * vs1, w[3] * vs1));
       }
       // ---- O^T += V^T P^T.  A transposed 8x8 of byte pairs holds, for one
       // pair of channels, two positions; the two channels go to rows r and
       // r + 8 of the product.
       const uint32_t vbase = slot + kStep * DP;
-      const int tok = (lane & 7) + (lane & 8);  // x4: positions 0-7, 8-15 of two chunks
 #pragma unroll
       for (int d2 = 0; d2 < DP / 32; ++d2) {
         if (2 * d2 * 16 >= P.c.head_dim) break;
-        uint4 v = ldsm_trans(vbase + chunk_at(tok, 2 * d2 + (lane >> 4)));
-        uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-        // A NaN code in a position that some row does not see must reach only
-        // the rows that do.
-        if (partial) {
-          const bool nan = has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w);
-          if (__any_sync(kFull, nan)) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t na[4];
+        for (int mt = 0; mt < kM; ++mt) {
+          // x4: positions 0-7, 8-15 of two chunks
+          const uint4 v = ldsm_trans(vbase + chunk_at(16 * mt + (lane & 15), 2 * d2 + (lane >> 4)));
+          uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+          // A NaN code in a position that some row does not see must reach only
+          // the rows that do.
+          if (partial) {
+            const bool nan = has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w);
+            if (__any_sync(kFull, nan)) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                // 1 where the code is a NaN, and 0 in the code's place.
-                uint32_t x = vw[2 * k + j], ones = 0u, keep = 0xffffffffu;
+              for (int k = 0; k < 2; ++k) {
+                uint32_t na[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                  if (((x >> (8 * b)) & 0x7fu) == 0x7fu) {
-                    ones |= 0x38u << (8 * b);  // e4m3 1.0
-                    keep &= ~(0xffu << (8 * b));
+                for (int j = 0; j < 2; ++j) {
+                  // 1 where the code is a NaN, and 0 in the code's place.
+                  uint32_t x = vw[2 * k + j], ones = 0u, keep = 0xffffffffu;
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    if (((x >> (8 * b)) & 0x7fu) == 0x7fu) {
+                      ones |= 0x38u << (8 * b);  // e4m3 1.0
+                      keep &= ~(0xffu << (8 * b));
+                    }
                   }
+                  vw[2 * k + j] = x & keep;
+                  na[2 * j] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0020));
+                  na[2 * j + 1] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0031));
                 }
-                vw[2 * k + j] = x & keep;
-                na[2 * j] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0020));
-                na[2 * j + 1] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0031));
-              }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float seen[4];
+                for (int nt = 0; nt < NT; ++nt) {
+                  float seen[4];
+                  const int p0 = base + 16 * mt + row_lane, p1 = p0 + 8;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  seen[c] = (p0 >= lo[nt][c] && p0 <= hi[nt][c]) ? 1.0f : 0.0f;
-                  seen[2 + c] = (p1 >= lo[nt][c] && p1 <= hi[nt][c]) ? 1.0f : 0.0f;
+                  for (int c = 0; c < 2; ++c) {
+                    seen[c] = (p0 >= lo[nt][c] && p0 <= hi[nt][c]) ? 1.0f : 0.0f;
+                    seen[2 + c] = (p1 >= lo[nt][c] && p1 <= hi[nt][c]) ? 1.0f : 0.0f;
+                  }
+                  const uint32_t b0 = transpose8x8(Pair<__half>::pack(seen[0], seen[1]));
+                  const uint32_t b1 = transpose8x8(Pair<__half>::pack(seen[2], seen[3]));
+                  float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma16816(hit, na[0], na[1], na[2], na[3], b0, b1);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (hit[i] > 0.0f) o[2 * d2 + k][nt][i] = __uint_as_float(0x7fffffffu);
                 }
-                const uint32_t b0 = transpose8x8(Pair<__half>::pack(seen[0], seen[1]));
-                const uint32_t b1 = transpose8x8(Pair<__half>::pack(seen[2], seen[3]));
-                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816(hit, na[0], na[1], na[2], na[3], b0, b1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (hit[i] > 0.0f) o[2 * d2 + k][nt][i] = __uint_as_float(0x7fffffffu);
               }
             }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t x = vw[2 * k], y = vw[2 * k + 1];
-          const uint32_t a0 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0020));
-          const uint32_t a1 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0031));
-          const uint32_t a2 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0020));
-          const uint32_t a3 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0031));
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x = vw[2 * k], y = vw[2 * k + 1];
+            const uint32_t a0 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0020));
+            const uint32_t a1 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0031));
+            const uint32_t a2 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0020));
+            const uint32_t a3 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0031));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[2 * d2 + k][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[2 * d2 + k][nt], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
+          }
         }
       }
       __syncwarp();  // the slot may be refilled
       issue();
     }
 
-    // ---- join the warps
+    // ---- the block's end, or the range's
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -439,92 +522,110 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         t += __shfl_xor_sync(kFull, t, 4);
         t += __shfl_xor_sync(kFull, t, 8);
         t += __shfl_xor_sync(kFull, t, 16);
-        const int r = nt * 8 + 2 * col_lane + c;
-        if (row_lane == 0) s_ml[warp * kRows + r] = make_float2(m[nt][c], t);
-        if (r < cu.k.rows) {
-          float* dst = s_o + (warp * kRows + r) * L::kPitch + 2 * row_lane;
+        l[nt][c] = t;
+      }
+    }
+    auto lse_of = [](float mm, float ll) {
+      return ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    };
+    // Where row r of the block goes (token j; false: not written).
+    auto place = [&](int r, int64_t* j, int* h) {
+      const int tok = (cu.k.row0 + r) / P.group;
+      *j = cu.q_off + tok;
+      *h = cu.head * P.group + cu.k.row0 + r - tok * P.group;
+      return r < cu.k.rows && *j < P.n_tokens;
+    };
+    if (whole) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          int64_t j;
+          int h;
+          if (!place(nt * 8 + 2 * col_lane + c, &j, &h)) continue;
+          const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
+          uint16_t* dst = P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + 2 * row_lane;
 #pragma unroll
           for (int d = 0; d < DP / 16; ++d)
-            *reinterpret_cast<float2*>(dst + d * 16) = make_float2(o[d][nt][c], o[d][nt][2 + c]);
+            if (d * 16 < P.c.head_dim)
+              *reinterpret_cast<uint32_t*>(dst + d * 16) =
+                  Pair<T>::pack(o[d][nt][c] * inv, o[d][nt][2 + c] * inv);
+          if (row_lane == 0 && P.lse != nullptr)
+            P.lse[j * P.q_heads + h] = lse_of(m[nt][c], l[nt][c]);
         }
       }
-    }
-    __syncthreads();
-    // Joins `count` partials (m, l, O) of one row and four channels.
-    struct Sum { float m, l; float4 o; };
-    auto store = [&](int row, int d, const Sum& a) {
-      const int tok = (cu.k.row0 + row) / P.group, g = cu.k.row0 + row - tok * P.group;
-      const int64_t j = cu.q_off + tok;
-      if (j >= P.n_tokens) return;
-      const int h = cu.head * P.group + g;
-      const float inv = a.l != 0.0f ? 1.0f / a.l : 0.0f;  // NaN stays NaN
-      *reinterpret_cast<uint2*>(P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + d) =
-          make_uint2(Pair<T>::pack(a.o.x * inv, a.o.y * inv), Pair<T>::pack(a.o.z * inv, a.o.w * inv));
-      if (d == 0 && P.lse != nullptr)
-        P.lse[j * P.q_heads + h] = a.l != 0.0f ? (a.m + log2f(a.l)) * kLn2 : -INFINITY;
-    };
-    auto add = [](Sum& a, float bm, float bl, const float4& bo) {
-      const float now = fmaxf(a.m, bm);
-      if (now == -INFINITY && bl == 0.0f) return;  // nothing seen there
-      const float ref = now == -INFINITY ? 0.0f : now;
-      const float fa = ex2(a.m - ref), fb = ex2(bm - ref);
-      a.m = now;
-      a.l = a.l * fa + bl * fb;
-      a.o.x = a.o.x * fa + bo.x * fb;
-      a.o.y = a.o.y * fa + bo.y * fb;
-      a.o.z = a.o.z * fa + bo.z * fb;
-      a.o.w = a.o.w * fa + bo.w * fb;
-    };
-    // Partial slots: 0 for a block that began in an earlier CTA, 1 for one
-    // that begins here and goes on.
-    const int64_t seg_first = range.last - cu.left;              // this segment's first unit
-    const int64_t block_first = seg_first - t_begin;       // the block's first unit
-    int64_t c0, c1;
-    block_ctas(range, block_first, cu.k.tiles, &c0, &c1);
-    const int quads = P.c.head_dim >> 2;
-    const int pf_floats = partial_floats(kRows, DP);
-    float* mine = P.partials + (2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * static_cast<int64_t>(pf_floats);
-    for (int i = tid; i < cu.k.rows * quads; i += kWarps * 32) {
-      const int row = i / quads, d = (i - row * quads) * 4;
-      Sum a{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    } else {
+      // Partial slots: 0 for a block that began in an earlier warp, 1 for one
+      // that begins here and goes on.
+      constexpr int kFloats = partial_floats(kRows, DP);
+      float* mine = P.partials + (2 * worker + (t_begin == 0 ? 1 : 0)) * kFloats;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w * kRows + row];
-        add(a, ml.x, ml.y, *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * L::kPitch + d));
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = nt * 8 + 2 * col_lane + c;
+          if (r >= cu.k.rows) continue;
+          float* dst = mine + r * DP + 2 * row_lane;
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d)
+            __stcg(reinterpret_cast<float2*>(dst + d * 16), make_float2(o[d][nt][c], o[d][nt][2 + c]));
+          if (row_lane == 0)
+            __stcg(reinterpret_cast<float2*>(mine + kRows * DP) + r, make_float2(m[nt][c], l[nt][c]));
+        }
       }
-      if (whole) {
-        store(row, d, a);
-      } else {
-        __stcg(reinterpret_cast<float4*>(mine + row * DP + d), a.o);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(mine + kRows * DP + 2 * row), make_float2(a.m, a.l));
-      }
-    }
-    if (!whole) {
-      // The last of the block's CTAs to get here joins its partials.
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(P.counters + c0, 1u);
-        const bool mine_last = before == static_cast<uint32_t>(c1 - c0);
-        if (mine_last) P.counters[c0] = 0u;  // ready for the next call
+      int64_t c0, c1;
+      block_workers(range, range.last - cu.left - t_begin, cu.k.tiles, &c0, &c1);
+      // This warp's group of the block: workers [g0, g1].
+      const int64_t first_group = c0 / kGroup, group = worker / kGroup;
+      const int groups = static_cast<int>(c1 / kGroup - first_group) + 1;
+      const int64_t g0 = max(c0, group * kGroup), g1 = min(c1, group * kGroup + kGroup - 1);
+      auto slot_of = [&](int64_t w) { return 2 * w + (w == c0 ? 1 : 0); };
+      // True in the last of n arrivals at a counter, which it resets.
+      auto last_of = [&](uint32_t* counter, int64_t n) {
         __threadfence();
-        *s_last = mine_last ? 1 : 0;
-      }
-      __syncthreads();
-      if (*s_last != 0) {
-        for (int i = tid; i < cu.k.rows * quads; i += kWarps * 32) {
-          const int row = i / quads, d = (i - row * quads) * 4;
-          Sum a{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* p = P.partials + (2 * c + (c == c0 ? 1 : 0)) * static_cast<int64_t>(pf_floats);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kRows * DP + 2 * row));
-            add(a, ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(p + row * DP + d)));
+        __syncwarp();
+        uint32_t is_last = 0u;
+        if (lane == 0) {
+          is_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(n - 1) ? 1u : 0u;
+          if (is_last != 0u) *counter = 0u;  // ready for the next call
+        }
+        is_last = __shfl_sync(kFull, is_last, 0);
+        __threadfence();
+        return is_last != 0u;
+      };
+      auto put_out = [&](int r, int d, float mm, float ll, const float4& x) {
+        int64_t j;
+        int h;
+        if (!place(r, &j, &h)) return;
+        const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+        *reinterpret_cast<uint2*>(P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + d) =
+            make_uint2(Pair<T>::pack(x.x * inv, x.y * inv), Pair<T>::pack(x.z * inv, x.w * inv));
+        if (d == 0 && P.lse != nullptr) P.lse[j * P.q_heads + h] = lse_of(mm, ll);
+      };
+      auto in_group = [&](int i) { return slot_of(g0 + i); };
+      const int members = static_cast<int>(g1 - g0) + 1;
+      if (last_of(P.counters + slot_of(g0), members)) {
+        if (groups == 1) {
+          join<DP, kRows>(P, cu.k.rows, members, in_group, put_out);
+        } else {
+          // The group's sum takes the place of its first partial (which this
+          // warp alone still reads, row by row ahead of the writes).
+          float* sum = P.partials + slot_of(g0) * kFloats;
+          join<DP, kRows>(P, cu.k.rows, members, in_group,
+                          [&](int r, int d, float mm, float ll, const float4& x) {
+                            __stcg(reinterpret_cast<float4*>(sum + r * DP + d), x);
+                            if (d == 0)
+                              __stcg(reinterpret_cast<float2*>(sum + kRows * DP) + r,
+                                     make_float2(mm, ll));
+                          });
+          if (last_of(P.counters + 2 * range.workers + c0, groups)) {
+            join<DP, kRows>(P, cu.k.rows, groups,
+                            [&](int i) { return slot_of(max(c0, (first_group + i) * kGroup)); },
+                            put_out);
           }
-          store(row, d, a);
         }
       }
     }
-    __syncthreads();  // the joining buffer is free again
     cu.left -= t_end - t_begin;
     if (cu.left > 0) next_block(P, cu, kShape);
   }
@@ -535,7 +636,7 @@ template <typename T, int DP, int NT>
 cudaError_t launch(const AttendParams& P, int ctas, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0ull};
   const auto kernel = attend_rows_kernel<T, DP, NT>;
-  const int bytes = smem_bytes<DP, NT>();
+  constexpr int bytes = Layout<DP>::kBytes;
   const cudaError_t e = set_smem_limit_once(done, kernel, bytes);
   if (e != cudaSuccess) return e;
   kernel<<<ctas, kWarps * 32, bytes, stream>>>(P);
@@ -557,7 +658,7 @@ int row_block(int max_q_len, int group) {
 }
 
 size_t row_partial_bytes(int rows, int ctas, int head_dim) {
-  return static_cast<size_t>(ctas) * 2 * partial_floats(rows, head_dim > 64 ? 128 : 64) * 4;
+  return static_cast<size_t>(ctas) * kWarps * 2 * partial_floats(rows, head_dim > 64 ? 128 : 64) * 4;
 }
 
 cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, cudaStream_t stream) {

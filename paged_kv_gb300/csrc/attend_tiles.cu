@@ -867,7 +867,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       if (there) store_lse(m, l);
     } else {
       int64_t c0, c1;
-      block_ctas(range, range.last - c.left - t_begin, c.k.tiles, &c0, &c1);
+      block_workers(range, range.last - c.left - t_begin, c.k.tiles, &c0, &c1);
       const int64_t size = partial_floats(d);
       auto partial = [&](int64_t cta) {
         const int64_t at = (2 * cta + (cta == c0 ? 1 : 0)) * 2 + t;
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
   Bars* B = reinterpret_cast<Bars*>(smem + L::bar);
   const int tid = threadIdx.x, warp = tid >> 5;
   Cursor c;
-  const Range range = find_range<kThreads>(P, unit_shape(), smem, &c);
+  const Range range = find_range<kThreads, 1>(P, unit_shape(), smem, &c);
   if (c.left == 0) return;
   if (P.c.head_dim % 32 != 0) {
     // The last step of Q K^T sums over 32 elements: zeros past head_dim.

@@ -3,8 +3,8 @@
 // The query rows of one (request, cache head) -- row = query token * group +
 // query head in the group -- are cut into blocks of `rows`, the positions that
 // a block sees into tiles of `tile`.  A unit is one tile of one block; a call's
-// units are ordered by request, head, block, tile, and every CTA takes an
-// equal contiguous range of them.  A kernel takes only the requests whose row
+// units are ordered by request, head, block, tile, and every worker takes an
+// equal contiguous range of them (a CTA, or a warp).  A kernel takes only the requests whose row
 // count lies in [min_rows, max_rows]; others are another kernel's.
 #pragma once
 
@@ -116,22 +116,25 @@ __device__ __forceinline__ void next_block(const AttendParams& P, Cursor& c, con
   c.k = make_block(P, c.r, c.block, u);
 }
 
-// A CTA's range of the call's units.
+// A worker's (CTA's or warp's) range of the call's units.
 struct Range {
-  int64_t total;   // the call's units
-  int64_t ctas;    // CTAs that have any
-  int64_t last;    // one past this CTA's last unit
+  int64_t total;    // the call's units
+  int64_t workers;  // workers that have any
+  int64_t last;     // one past this worker's last unit
 };
 
-// Finds this CTA's range and sets *c to its first unit (c->left 0: none).
-// All THREADS of the CTA take part; `scratch` is 512 bytes of shared memory,
-// free again on return.  Block 0 reports the requests' errors.
-template <int THREADS>
+// Finds this worker's range and sets *c to its first unit (c->left 0: none).
+// A CTA has WORKERS of them (1, or one a warp).  All THREADS of the CTA take
+// part; `scratch` is THREADS * 16 + 16 bytes of shared memory, free again on
+// return.  Block 0 reports the requests' errors.
+template <int THREADS, int WORKERS>
 __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scratch, Cursor* c) {
   constexpr int kW = THREADS / 32;
+  static_assert(WORKERS == 1 || WORKERS == kW, "a CTA's workers");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long* s_w = static_cast<long long*>(scratch);
-  long long* s_at = s_w + 2 * kW;
+  // Units and tokens before each thread's requests.
+  long long* s_u = static_cast<long long*>(scratch);
+  long long* s_t = s_u + THREADS;
   const int per = (P.B + THREADS - 1) / THREADS;
   const int i0 = min(P.B, tid * per), i1 = min(P.B, i0 + per);
   long long units = 0, toks = 0;
@@ -148,68 +151,74 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
     const long long a = __shfl_up_sync(kFull, ui, o), b = __shfl_up_sync(kFull, ti, o);
     if (lane >= o) ui += a, ti += b;
   }
-  if (lane == 31) s_w[warp] = ui, s_w[kW + warp] = ti;
+  if (lane == 31) s_u[warp] = ui, s_t[warp] = ti;
   __syncthreads();
   long long ubase = ui - units, tbase = ti - toks, total = 0, ntok = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kW; ++w) {
-    if (w < warp) ubase += s_w[w], tbase += s_w[kW + w];
-    total += s_w[w], ntok += s_w[kW + w];
+    if (w < warp) ubase += s_u[w], tbase += s_t[w];
+    total += s_u[w], ntok += s_t[w];
   }
+  __syncthreads();
+  s_u[tid] = ubase;
+  s_t[tid] = tbase;
   if (blockIdx.x == 0 && P.status != nullptr) {
     if (tid == 0 && ntok > P.n_tokens) bad |= PKV_ST_TOKEN_CAP;
     if (bad != 0) atomicOr(P.status, bad);
   }
+  __syncthreads();
   Range g;
   g.total = total;
-  g.ctas = min(static_cast<long long>(gridDim.x), total);
-  if (blockIdx.x >= g.ctas) {
-    c->left = 0;
-    g.last = total;
-    return g;
-  }
-  const long long first = blockIdx.x * total / g.ctas;
-  g.last = (blockIdx.x + 1ll) * total / g.ctas;
-  if (ubase <= first && first < ubase + units) {
-    for (int i = i0; i < i1; ++i) {
-      const Request r = load_request(P, i);
-      const long long n = request_units(P, r, u);
-      if (first < ubase + n) {
-        s_at[0] = i;
-        s_at[1] = first - ubase;
-        s_at[2] = tbase;
+  g.workers = min(static_cast<long long>(gridDim.x) * WORKERS, total);
+  g.last = total;
+  c->left = 0;
+  const long long me = static_cast<long long>(blockIdx.x) * WORKERS + (WORKERS == 1 ? 0 : warp);
+  if (me < g.workers) {
+    const long long first = me * total / g.workers;
+    g.last = (me + 1) * total / g.workers;
+    // The last thread whose requests begin at or before `first` (threads
+    // without units begin where the next one does, and are passed over).
+    int k = 0;
+#pragma unroll 1
+    for (int t = lane; t < THREADS; t += 32) {
+      if (s_u[t] <= first) k = t;
+    }
+    k = __reduce_max_sync(kFull, k);
+    long long at = first - s_u[k];
+    c->q_off = s_t[k];
+    c->left = g.last - first;
+    c->req = k * per;
+    for (;;) {
+      c->r = load_request(P, c->req);
+      const long long n = request_units(P, c->r, u);
+      if (at < n) {
+        const long long per_head = n / P.c.kv_heads;
+        c->head = static_cast<int>(at / per_head);
+        at -= c->head * per_head;
         break;
       }
-      ubase += n;
-      tbase += r.q_len;
+      at -= n;
+      c->q_off += c->r.q_len;
+      ++c->req;
     }
+    c->block = 0;
+    for (;;) {
+      c->k = make_block(P, c->r, c->block, u);
+      if (at < c->k.tiles) break;
+      at -= c->k.tiles;
+      ++c->block;
+    }
+    c->tile = static_cast<int>(at);
   }
-  __syncthreads();
-  c->req = static_cast<int>(s_at[0]);
-  c->q_off = s_at[2];
-  c->left = g.last - first;
-  c->r = load_request(P, c->req);
-  long long at = s_at[1];
-  const long long per_head = request_units(P, c->r, u) / P.c.kv_heads;
-  c->head = static_cast<int>(at / per_head);
-  at -= c->head * per_head;
-  c->block = 0;
-  for (;;) {
-    c->k = make_block(P, c->r, c->block, u);
-    if (at < c->k.tiles) break;
-    at -= c->k.tiles;
-    ++c->block;
-  }
-  c->tile = static_cast<int>(at);
   __syncthreads();
   return g;
 }
 
-// The CTAs that hold a block's first and last unit, given its first unit.
-__device__ __forceinline__ void block_ctas(const Range& g, int64_t block_first, int tiles,
-                                           int64_t* c0, int64_t* c1) {
-  *c0 = ((block_first + 1) * g.ctas - 1) / g.total;
-  *c1 = ((block_first + tiles) * g.ctas - 1) / g.total;
+// The workers that hold a block's first and last unit, given its first unit.
+__device__ __forceinline__ void block_workers(const Range& g, int64_t block_first, int tiles,
+                                              int64_t* c0, int64_t* c1) {
+  *c0 = ((block_first + 1) * g.workers - 1) / g.total;
+  *c1 = ((block_first + tiles) * g.workers - 1) / g.total;
 }
 
 }  // namespace pkv
