@@ -421,9 +421,9 @@ int pkv_check_free_list(const int32_t* free_slots, int64_t free_count, int page_
  * [2^-64, 2^119]; pkv_append_kv writes powers of two.
  *   Requirements: k, v 16-byte aligned; the strides multiples of 16;
  *   head_dim a multiple of 16 in [16, PKV_MAX_HEAD_DIM]; page_size and
- *   kv_heads >= 1; num_pages * page_size < 2^31; page_stride <= 2^40 and
- *   num_pages * page_stride, page_size * token_stride and
- *   kv_heads * head_stride at most 2^46.
+ *   kv_heads >= 1; num_pages * page_size < 2^31; num_pages * page_stride at
+ *   most 2^35 (32 GiB of keys, and as much of values, a layer), page_size *
+ *   token_stride and kv_heads * head_stride at most 2^34.
  */
 typedef struct {
   void* k;

@@ -78,6 +78,9 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   AttendParams P;
   P.c = *cache;
   P.page_div = Divider::by(static_cast<uint32_t>(cache->page_size));
+  P.page_step = static_cast<uint32_t>(cache->page_stride / 16);
+  P.token_step = static_cast<uint32_t>(cache->token_stride / 16);
+  P.head_step = static_cast<uint32_t>(cache->head_stride / 16);
   P.q = static_cast<const uint16_t*>(q);
   P.out = static_cast<uint16_t*>(out);
   P.lse = lse;

@@ -32,6 +32,7 @@ struct Divider {
 struct AttendParams {
   pkv_kv_cache c;
   Divider page_div;            // by c.page_size
+  uint32_t page_step, token_step, head_step;  // c's strides in 16 bytes
   const uint16_t* q;
   uint16_t* out;
   float* lse;                  // or nullptr

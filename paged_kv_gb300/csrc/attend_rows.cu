@@ -18,10 +18,11 @@
 // on mma.m16n8k16 with fp16 inputs: e4m3 codes are exact in fp16, and a query
 // is scaled to at most 2 by a power of two, so the products are exact.  Scores
 // take the page's key scale in fp32.  Weights carry the page's value scale:
-// with m the running maximum of s + log2(vs), p = 2^(s - m) vs <= 2^8 goes to
-// fp16 (11 bits), and l sums 2^(s - m) in fp32, so neither over- nor
-// underflows for any scales.  m moves only when it would rise by more than 8:
-// sums stay far below fp16's and fp32's limits and most units rescale nothing.
+// p = 2^3 2^(s - m) vs goes to fp16 (11 bits), l sums 2^(s - m) in fp32, so
+// neither over- nor underflows for any scales.  The reference m is not the
+// running maximum: it is taken from a row's first positions and moves only
+// where the weights under it sum to more than 2^15.  So a unit needs no maximum
+// over its lanes, and few units rescale.
 //
 // Bound: bytes.  Each cached byte is read once (2 D per position and head).
 
@@ -47,7 +48,8 @@ constexpr int kStep = 32;                // positions a warp takes at a time: on
 constexpr int kStages = 2;               // ring slots of a warp
 constexpr int kGroup = 16;               // warps whose partials are joined first
 static_assert(kStep == 32, "a lane looks up one position");
-constexpr float kLazy = 8.0f;            // log2 of how far sums may outgrow their reference
+constexpr float kUnit = 8.0f;            // a weight in fp16 is this times 2^(s - m) vs
+constexpr float kLimit = 32768.0f;       // sum of such weights that moves m
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int DP>
@@ -222,45 +224,54 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   const int chunks = P.c.head_dim >> 4;
   int issued = 0;
 
+  // The location of this lane's position in the next unit, read a unit ahead.
+  auto look = [&]() -> int {
+    const int tok = ld.k.start + ld.tile * kStep + lane;
+    const bool in = ld.left > 0 && tok >= ld.k.lo && tok < ld.k.end;
+    return in ? P.page_table[ld.r.table_row * P.pt_cols + tok] : -1;
+  };
+  int loc = look();
+  constexpr int kPer = 32 / kChunks;  // positions a round of the warp's copies covers
+  const int ch = lane % kChunks;
   // Copies the next unit, or commits an empty group.
   auto issue = [&]() {
     if (ld.left > 0) {
-      const int base = ld.k.start + ld.tile * kStep;
-      {
-        const uint32_t slot = ring + (issued % kStages) * (L::kSlot + L::kScales);
-        ++issued;
-        const int tok = base + lane;
-        bool valid = tok >= ld.k.lo && tok < ld.k.end;
-        int loc = 0;
-        if (valid) loc = P.page_table[ld.r.table_row * P.pt_cols + tok];
-        if (loc < 0 || loc >= slots) {
-          if (P.status != nullptr) atomicOr(P.status, PKV_ST_ROW_OOB);
-          loc = 0;
-          valid = false;
-        }
-        const int page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(loc)));
-        const int64_t at = page * P.c.page_stride + (loc - page * ps) * P.c.token_stride +
-                           ld.head * P.c.head_stride;
-        const int64_t sc = static_cast<int64_t>(page) * P.c.kv_heads + ld.head;
-        cp_async4_zfill(slot + L::kSlot + lane * 4, P.c.k_scale + sc, valid);
-        cp_async4_zfill(slot + L::kSlot + kStep * 4 + lane * 4, P.c.v_scale + sc, valid);
-        const unsigned ok = __ballot_sync(kFull, valid);
-        constexpr int kPer = 32 / kChunks;  // positions a round of the warp covers
-        const int ch = lane % kChunks;
+      const uint32_t slot = ring + (issued % kStages) * (L::kSlot + L::kScales);
+      ++issued;
+      const bool valid = loc >= 0 && loc < slots;
+      if (!valid) {
+        const int tok = ld.k.start + ld.tile * kStep + lane;
+        if (tok >= ld.k.lo && tok < ld.k.end && P.status != nullptr)
+          atomicOr(P.status, PKV_ST_ROW_OOB);
+        loc = 0;
+      }
+      const int page = static_cast<int>(P.page_div.divide(static_cast<uint32_t>(loc)));
+      // In units of 16 bytes: 32 bits reach 64 GiB.
+      const uint32_t at = static_cast<uint32_t>(page) * P.page_step +
+                          static_cast<uint32_t>(loc - page * ps) * P.token_step +
+                          static_cast<uint32_t>(ld.head) * P.head_step;
+      const int64_t sc = static_cast<int64_t>(page) * P.c.kv_heads + ld.head;
+      cp_async4_zfill(slot + L::kSlot + lane * 4, P.c.k_scale + sc, valid);
+      cp_async4_zfill(slot + L::kSlot + kStep * 4 + lane * 4, P.c.v_scale + sc, valid);
+      const unsigned ok = __ballot_sync(kFull, valid) >> (lane / kChunks);
+      const uint32_t dst = slot + chunk_at(lane / kChunks, ch);
 #pragma unroll
-        for (int i = 0; i < kStep / kPer; ++i) {
-          const int t = i * kPer + lane / kChunks;
-          const int64_t off = __shfl_sync(kFull, at, t);
-          if (ch < chunks) {
-            const bool v = (ok >> t) & 1u;
-            const uint32_t dst = slot + chunk_at(t, ch);
-            cp_async16_zfill(dst, static_cast<const uint8_t*>(P.c.k) + off + ch * 16, v);
-            cp_async16_zfill(dst + kStep * DP, static_cast<const uint8_t*>(P.c.v) + off + ch * 16, v);
-          }
+      for (int i = 0; i < kStep / kPer; ++i) {
+        const uint32_t from = __shfl_sync(kFull, at, i * kPer + lane / kChunks);
+        if (ch < chunks) {
+          const bool v = (ok >> (i * kPer)) & 1u;
+          const uint64_t off = static_cast<uint64_t>(from) * 16 + ch * 16;
+          // (The swizzle repeats every 8 positions.)
+          const uint32_t to = kPer == 8 ? dst + i * 8 * DP
+                              : (i & 1) ? slot + chunk_at(kPer + lane / kChunks, ch) + (i >> 1) * 8 * DP
+                                        : dst + (i >> 1) * 8 * DP;
+          cp_async16_zfill(to, static_cast<const uint8_t*>(P.c.k) + off, v);
+          cp_async16_zfill(to + kStep * DP, static_cast<const uint8_t*>(P.c.v) + off, v);
         }
       }
       --ld.left;
       if (++ld.tile >= ld.k.tiles && ld.left > 0) next_block(P, ld, kShape);
+      loc = look();
     }
     cp_async_commit();
   };
@@ -325,9 +336,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         const int r = nt * 8 + 2 * col_lane + c;
         cf[nt][c] = P.scale_log2 / __shfl_sync(kFull, unit, (2 * col_lane + c) * 4);
         const int p = cu.r.cached + (cu.k.row0 + r) / P.group;
-        hi[nt][c] = r < cu.k.rows ? min(p, cu.k.end - 1) : -1;
-        lo[nt][c] = cu.r.begin;
-        if (P.window > 0) lo[nt][c] = max(lo[nt][c], p - P.window + 1);
+        // (A row that is not there sees everything: it must not keep m waiting.)
+        hi[nt][c] = r < cu.k.rows ? min(p, cu.k.end - 1) : INT32_MAX;
+        lo[nt][c] = r < cu.k.rows ? cu.r.begin : 0;
+        if (P.window > 0 && r < cu.k.rows) lo[nt][c] = max(lo[nt][c], p - P.window + 1);
         if (r < cu.k.rows) {
           all_hi = min(all_hi, hi[nt][c]);
           all_lo = max(all_lo, lo[nt][c]);
@@ -378,21 +390,17 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       }
       // ---- softmax.  Position i of this thread: base + 8 i + row_lane.
       const uint32_t sc = slot + L::kSlot + row_lane * 4;
-      float ks[2 * kM], vs[2 * kM], lv[2 * kM];
+      float ks[2 * kM], vs[2 * kM];  // vs times kUnit
 #pragma unroll
       for (int i = 0; i < 2 * kM; ++i) {
         ks[i] = lds32(sc + 32 * i);
-        vs[i] = lds32(sc + kStep * 4 + 32 * i);
-        lv[i] = lg2(fmaxf(vs[i], 5.42101086e-20f));
+        vs[i] = lds32(sc + kStep * 4 + 32 * i) * kUnit;
       }
       const bool partial = base < all_lo || base + kStep - 1 > all_hi;  // uniform
-      float top[NT][2];
-      bool rise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float t = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 2 * kM; ++i) {
             float& x = s[i >> 1][nt][2 * (i & 1) + c];
@@ -401,21 +409,46 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
               const int p = base + 8 * i + row_lane;
               if (p < lo[nt][c] || p > hi[nt][c]) x = -INFINITY;
             }
-            t = fmaxf(t, x + lv[i]);
           }
-          t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
-          t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
-          t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
-          top[nt][c] = t;
-          rise = rise || t > m[nt][c] + kLazy;
         }
       }
-      if (__any_sync(kFull, rise)) {
+      // Weights under the references as they are; where their sum passes the
+      // limit, or a row has no reference yet, m moves and they are done again.
+      float pw[kM][NT][4], part[NT][2];
+      for (bool moved = false;; moved = true) {
+        bool past = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float now = fmaxf(m[nt][c], top[nt][c]);
+            const float ref = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
+            float held = 0.0f;
+            part[nt][c] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * kM; ++i) {
+              const float w = ex2(s[i >> 1][nt][2 * (i & 1) + c] - ref);
+              part[nt][c] += w;
+              const float x = w * vs[i];
+              held += x;
+              pw[i >> 1][nt][2 * (i & 1) + c] = x;
+            }
+            past = past || !(held <= kLimit) || m[nt][c] == -INFINITY;
+          }
+        }
+        if (moved || !__any_sync(kFull, past)) break;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float t = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2 * kM; ++i)
+              t = fmaxf(t, s[i >> 1][nt][2 * (i & 1) + c] + lg2(fmaxf(vs[i], 5.42101086e-20f)));
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+            // (The same in all lanes that hold the row's columns.)
+            const float now = fmaxf(m[nt][c], t);
             const float f = now == -INFINITY ? 1.0f : ex2(m[nt][c] - now);
             m[nt][c] = now;
             l[nt][c] *= f;
@@ -430,16 +463,12 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       uint32_t pf[kM][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-        const float r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+        l[nt][0] += part[nt][0];
+        l[nt][1] += part[nt][1];
 #pragma unroll
-        for (int i = 0; i < 2 * kM; ++i) {
-          const float a = ex2(s[i >> 1][nt][2 * (i & 1)] - r0);
-          const float b = ex2(s[i >> 1][nt][2 * (i & 1) + 1] - r1);
-          l[nt][0] += a;
-          l[nt][1] += b;
-          pf[i >> 1][nt][i & 1] = transpose8x8(Pair<__half>::pack(a * vs[i], b * vs[i]));
-        }
+        for (int i = 0; i < 2 * kM; ++i)
+          pf[i >> 1][nt][i & 1] = transpose8x8(Pair<__half>::pack(pw[i >> 1][nt][2 * (i & 1)],
+                                                                  pw[i >> 1][nt][2 * (i & 1) + 1]));
       }
       // ---- O^T += V^T P^T.  A transposed 8x8 of byte pairs holds, for one
       // pair of channels, two positions; the two channels go to rows r and
@@ -498,11 +527,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t x = vw[2 * k], y = vw[2 * k + 1];
-            const uint32_t a0 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0020));
-            const uint32_t a1 = e4m3x2_to_f16x2(__byte_perm(x, 0u, 0x0031));
-            const uint32_t a2 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0020));
-            const uint32_t a3 = e4m3x2_to_f16x2(__byte_perm(y, 0u, 0x0031));
+            const uint32_t x = __byte_perm(vw[2 * k], 0u, 0x3120);
+            const uint32_t y = __byte_perm(vw[2 * k + 1], 0u, 0x3120);
+            const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_to_f16x2(x >> 16);
+            const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma16816(o[2 * d2 + k][nt], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
@@ -543,7 +571,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           int64_t j;
           int h;
           if (!place(nt * 8 + 2 * col_lane + c, &j, &h)) continue;
-          const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
+          const float inv = l[nt][c] != 0.0f ? (1.0f / kUnit) / l[nt][c] : 0.0f;  // NaN stays NaN
           uint16_t* dst = P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + 2 * row_lane;
 #pragma unroll
           for (int d = 0; d < DP / 16; ++d)
@@ -597,7 +625,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         int64_t j;
         int h;
         if (!place(r, &j, &h)) return;
-        const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+        const float inv = ll != 0.0f ? (1.0f / kUnit) / ll : 0.0f;
         *reinterpret_cast<uint2*>(P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + d) =
             make_uint2(Pair<T>::pack(x.x * inv, x.y * inv), Pair<T>::pack(x.z * inv, x.w * inv));
         if (d == 0 && P.lse != nullptr) P.lse[j * P.q_heads + h] = lse_of(mm, ll);

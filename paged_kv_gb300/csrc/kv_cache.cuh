@@ -44,8 +44,10 @@ inline int cache_error(const pkv_kv_cache* c) {
                 PKV_MAX_HEAD_DIM);
   const int64_t strides[3] = {c->page_stride, c->token_stride, c->head_stride};
   const int64_t counts[3] = {c->num_pages, c->page_size, c->kv_heads};
+  // Kernels reach a code by 32 bits of 16-byte steps: 64 GiB in all.
+  const int64_t spans[3] = {int64_t{1} << 35, int64_t{1} << 34, int64_t{1} << 34};
   for (int i = 0; i < 3; ++i) {
-    if (strides[i] < 0 || strides[i] % 16 != 0 || strides[i] > (int64_t{1} << 46) / counts[i])
+    if (strides[i] < 0 || strides[i] % 16 != 0 || strides[i] > spans[i] / counts[i])
       return fail(PKV_EINVAL, "cache stride %lld is not a multiple of 16 within the limits",
                   (long long)strides[i]);
   }
