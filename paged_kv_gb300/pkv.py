@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libpkv.so`` (the C ABI in ``include/pkv.h``).
+"""Thin binding of ``libpkv.so`` (the C ABI in ``include/pkv.h``): by ctypes, and for
+the serving operators by ``_binding.so`` (``csrc/binding.cpp``).
 
 Argument marshalling only: every step of the sampler, the write-back and the
 page fill runs in the library's CUDA kernels.  PyTorch supplies device memory
@@ -508,6 +509,7 @@ class KVCache:
         self._struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                       v_scale.data_ptr(), pages, *strides, ps, heads, dim, 0)
         self._ref = ctypes.addressof(self._struct)
+        self._index = k.device.index
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
@@ -527,27 +529,18 @@ class KVCache:
         return cls(codes(), codes(), scales(), scales())
 
 
-def _half_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return PKV_BF16
-    if t.dtype == torch.float16:
-        return PKV_FP16
-    raise TypeError(f"{name} dtype {t.dtype} is not bf16 or fp16")
+_binding = None
 
 
-def _rows(t: torch.Tensor, dtype: torch.dtype, shape, name: str):
-    """(pointer, token stride, head stride) of a [tokens, heads, head_dim] CUDA tensor."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"{name} must have unit last stride")
-    # The stride of a dimension of one is never used, and torch leaves any value in it.
-    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+def _bind():
+    """The compiled binding of the serving operators (paged_kv_gb300/_binding.so)."""
+    global _binding
+    if _binding is None:
+        load()
+        from . import _binding as module
+
+        _binding = module
+    return _binding
 
 
 def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -560,35 +553,12 @@ def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch
     ``positions`` under ``cos_sin`` [max_pos, rot_dim] (cosines, then sines; None: no
     rotation).  Returns the rotated queries (``q_out``, allocated here if not given;
     None without ``q``).  See include/pkv.h."""
-    lib = load()
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, kv_heads, head_dim]")
-    n = k.shape[0]
-    shape = (n, cache.kv_heads, cache.head_dim)
-    code = _half_code(k, "k")
-    max_pos = rot = 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_pos, rot_dim]")
-        max_pos, rot = cos_sin.shape
-    q_args = (None, 0, 0, 0, None, 0, 0)
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [tokens, q_heads, head_dim]")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        q_shape = (n, q.shape[1], cache.head_dim)
-        q_args = (*_rows(q, k.dtype, q_shape, "q"), q.shape[1],
-                  *_rows(q_out, k.dtype, q_shape, "q_out"))
-    elif q_out is not None:
-        raise ValueError("q_out given without q")
-    rc = lib.pkv_append_kv(
-        cache._ref, *_rows(k, k.dtype, shape, "k"), *_rows(v, k.dtype, shape, "v"), code, n,
-        _dev(total_tokens, torch.int64, "total_tokens", 1),
-        _dev(positions, torch.int32, "positions", n), _dev(out_loc, torch.int32, "out_loc", n),
-        _dev(cos_sin, torch.float32, "cos_sin"), max_pos, rot, int(interleaved), *q_args,
-        _dev(status, torch.int32, "status", 1), _stream(stream, cache.device))
-    _check(rc)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rc = (_binding or _bind()).append_kv(cache._ref, cache._index, k, v, positions, out_loc, cos_sin,
+                                         interleaved, q, q_out, total_tokens, status, stream)
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -601,15 +571,6 @@ def paged_attention_workspace_bytes(B: int, n_tokens: int, max_q_len: int, q_hea
     return int(load().pkv_paged_attention_workspace_bytes(int(B), int(n_tokens), int(max_q_len),
                                                           int(q_heads), int(kv_heads),
                                                           int(head_dim)))
-
-
-def _attention_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    """As ``_workspace``: one zero-initialised buffer per device, for one stream at a time."""
-    ws = _attention_workspaces.get(device.index)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _attention_workspaces[device.index] = ws
-    return ws
 
 
 def paged_attention(q: torch.Tensor, cache: KVCache, cached_len: torch.Tensor,
@@ -625,34 +586,22 @@ def paged_attention(q: torch.Tensor, cache: KVCache, cached_len: torch.Tensor,
     stream) defaults to a buffer cached per device.  Returns ``out`` (allocated here if
     not given); ``lse`` [n, q_heads] fp32 receives the log-sum-exp if given.  See
     include/pkv.h."""
-    lib = load()
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, q_heads, head_dim]")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be 2-D")
-    code = _half_code(q, "q")
-    n, heads, dim = q.shape
-    shape = (n, heads, cache.head_dim)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    B = cached_len.numel()
-    max_q_len = int(max_q_len)
-    need = lib.pkv_paged_attention_workspace_bytes(B, n, max_q_len, heads, cache.kv_heads, dim)
-    if workspace is None:
-        workspace = _attention_workspace(cache.device, need)
-    elif workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
-    rc = lib.pkv_paged_attention(
-        cache._ref, *_rows(q, q.dtype, shape, "q"), heads, code, n,
-        *_rows(out, q.dtype, shape, "out"), _dev(lse, torch.float32, "lse", n * heads),
-        _dev(cached_len, torch.int32, "cached_len", B),
-        _dev(device_len, torch.int32, "device_len", B),
-        _dev(table_idx, torch.int32, "table_idx", B), _dev(kv_begin, torch.int32, "kv_begin", B),
-        B, max_q_len, _dev(page_table, torch.int32, "page_table"), page_table.shape[0],
-        page_table.shape[1], dim ** -0.5 if sm_scale is None else float(sm_scale), int(window),
-        _dev(status, torch.int32, "status", 1), workspace.data_ptr(), workspace.numel(),
-        _stream(stream, cache.device))
-    _check(rc)
+    cached = workspace is None
+    if cached:
+        workspace = _attention_workspaces.get(cache._index)
+    call = (_binding or _bind()).paged_attention
+    rc = call(cache._ref, cache._index, q, out, lse, cached_len, device_len, table_idx, kv_begin,
+              max_q_len, page_table, sm_scale, window, status, workspace, stream, cached)
+    if rc:
+        if rc < -1000:  # as ``_workspace``: one zero-initialised buffer per device
+            workspace = torch.zeros(-1000 - rc, dtype=torch.uint8, device=cache.device)
+            _attention_workspaces[cache._index] = workspace
+            rc = call(cache._ref, cache._index, q, out, lse, cached_len, device_len, table_idx,
+                      kv_begin, max_q_len, page_table, sm_scale, window, status, workspace, stream,
+                      False)
+        _check(rc)
     return out
 
 
@@ -673,48 +622,11 @@ def adjust_logits(logits: torch.Tensor, out: Optional[torch.Tensor] = None,
     history in ``token_pool``, then sparse biases, then a grammar bit mask
     ([B, ceil(V / 32)] int32), into ``out`` (None: in place).  Returns it.  See
     include/pkv.h."""
-    lib = load()
-    if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
-        raise ValueError("logits must be a 2-D CUDA tensor with unit column stride")
-    if logits.dtype == torch.bfloat16:
-        dcode = PKV_BF16
-    elif logits.dtype == torch.float32:
-        dcode = PKV_FP32
-    else:
-        raise TypeError(f"logits dtype {logits.dtype} is not fp32 or bf16")
-    B, V = logits.shape
     if out is None:
         out = logits
-    elif (out.dim() != 2 or not out.is_cuda or out.dtype != logits.dtype
-          or out.shape != logits.shape or out.stride(1) != 1):
-        raise ValueError("out must be a CUDA tensor of the logits' shape and dtype with unit "
-                         "column stride")
-    pool_rows = pool_cols = 0
-    if token_pool is not None:
-        if token_pool.dim() != 2:
-            raise ValueError("token_pool must be 2-D")
-        pool_rows, pool_cols = token_pool.shape
-    n_bias = 0
-    if bias_ids is not None:
-        n_bias = bias_ids.numel()
-    mask_stride = 0
-    if mask is not None:
-        if (mask.dim() != 2 or not mask.is_cuda or mask.dtype != torch.int32
-                or mask.stride(1) != 1 or mask.shape[0] < B or mask.shape[1] < (V + 31) // 32):
-            raise ValueError(f"mask must be a CUDA int32 tensor [{B}, {(V + 31) // 32}] with unit "
-                             "column stride")
-        mask_stride = mask.stride(0)
-    rc = lib.pkv_adjust_logits(
-        logits.data_ptr(), logits.stride(0), dcode, B, V, out.data_ptr(), out.stride(0),
-        _dev(token_pool, torch.int32, "token_pool"), pool_rows, pool_cols,
-        _dev(table_idx, torch.int32, "table_idx", B), _dev(prompt_len, torch.int32, "prompt_len", B),
-        _dev(device_len, torch.int32, "device_len", B),
-        _dev(repetition, torch.float32, "repetition", B),
-        _dev(presence, torch.float32, "presence", B),
-        _dev(frequency, torch.float32, "frequency", B),
-        _dev(bias_ptr, torch.int32, "bias_ptr", B + 1), _dev(bias_ids, torch.int32, "bias_ids"),
-        _dev(bias_values, torch.float32, "bias_values", n_bias), n_bias,
-        mask.data_ptr() if mask is not None else None, mask_stride,
-        _dev(status, torch.int32, "status", 1), _stream(stream, logits.device))
-    _check(rc)
+    rc = (_binding or _bind()).adjust_logits(
+        logits, out, token_pool, table_idx, prompt_len, device_len, repetition, presence, frequency,
+        bias_ptr, bias_ids, bias_values, mask, status, stream)
+    if rc:
+        _check(rc)
     return out

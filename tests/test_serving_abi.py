@@ -121,5 +121,24 @@ def test_binding_refuses_wrong_tensors():
         pkv.KVCache(f8, f8, s, s)  # not on the GPU
     with pytest.raises(ValueError):
         pkv.adjust_logits(torch.zeros(2, 8))
+
+
+class HostCache:
+    """Stands in for a KVCache where a call is refused before any launch."""
+
+    def __init__(self):
+        self._struct = cache()
+        self._ref, self._index = ctypes.addressof(self._struct), 0
+        self.device = torch.device("cpu")
+
+
+def test_binding_checks_every_tensor_before_the_call():
+    c = HostCache()
+    x, i = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for bad in (x, x.float(), 5, None):
+        with pytest.raises(TypeError):
+            pkv.append_kv(c, bad, x, i, i)
+        with pytest.raises(TypeError):
+            pkv.paged_attention(bad if isinstance(bad, torch.Tensor) else x, c, i, i, i, i, 1)
     with pytest.raises(TypeError):
-        pkv._half_code(torch.zeros(1), "k")
+        pkv._bind().append_kv(c._ref, 0)
