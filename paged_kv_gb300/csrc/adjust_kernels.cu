@@ -18,7 +18,17 @@
 // Cells are 16 bits where the row's made tokens number at most 16383 (a
 // 14-bit count), else 32 bits, in two passes of half a slice.
 //
-// Bound: bytes (out of place: one read and one write of the logits).
+// Bound: bytes (out of place: one read and one write of the logits).  For 256 x
+// 151936 bf16 (histories to 2512 tokens, 64 biases a row, a third of the rows
+// masked) 44 us, 3.7 TB/s; for 1024 x 256000 bf16 (histories to 36863 tokens,
+// 300 biases a row) 415 us, 2.8 TB/s, of which the histories take half: every
+// slice of a row reads them all (150 us, the latency of those reads more than
+// their count), atomics on the frequent tokens 40, penalties in the stream 60.
+// Measured against this for the second size: two CTAs an SM with 96 KB of cells
+// 478; the slices of a row as a cluster that counts each token once, in the
+// owner's cells, 748; the history in a hash table by a kernel of its own and
+// the named tokens written one by one 977 (they touch most of the row's
+// sectors again).
 
 #include <cuda_runtime.h>
 
@@ -39,9 +49,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kUnroll = 4;
-constexpr int kCellBytes = 96 * 1024;  // shared memory of the cells: two CTAs an SM
+constexpr int kCellBytes = 64 * 1024;  // shared memory of the cells: three CTAs an SM
 constexpr int kMaxCount16 = 16383;
-constexpr int kBiasCap = 512;          // gathered biases of a slice
+constexpr int kBiasCap = kThreads;     // gathered biases of a slice
 
 struct AdjustParams {
   const void* logits;
@@ -96,7 +106,7 @@ __device__ __forceinline__ uint32_t cell_take(uint32_t* cells, int i) {
 
 // One row as its CTAs see it.
 struct Row {
-  float rep, pres, freq;
+  float rep, inv, pres, freq;  // inv = 1 / rep
   int len, prompt;
   const int32_t* hist;
   int bias_begin, bias_end;
@@ -105,10 +115,14 @@ struct Row {
 
 template <int BITS>
 __device__ __forceinline__ float penalise(const Row& r, float x, uint32_t cell) {
-  const uint32_t count = cell & CellOf<BITS>::kCount;
-  if (cell != 0u) x = x > 0.0f ? x / r.rep : x * r.rep;
-  if (count != 0u) x = x - r.freq * static_cast<float>(count) - r.pres;
-  return x;
+  // A product with the reciprocal: both are rounded to 32 bits, so it is within
+  // 1.5 units in the last place of the quotient (a division for each element of
+  // the stream costs 20 times the instructions).  Without branches: the choice
+  // at the end leaves an unnamed token as it is, whatever the penalties hold.
+  const float count = static_cast<float>(cell & CellOf<BITS>::kCount);
+  float y = x * (x > 0.0f ? r.inv : r.rep);
+  y = count > 0.0f ? y - r.freq * count - r.pres : y;
+  return cell != 0u ? y : x;
 }
 
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
@@ -128,85 +142,137 @@ template <> __device__ __forceinline__ uint32_t minus_inf_word<__nv_bfloat16>() 
 // The tokens [v0, v1) of one row.
 template <typename T, int BITS, bool INPLACE>
 __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T* out, int v0,
-                             int v1, uint32_t* cells, int* s_id, float* s_val, int* s_count) {
+                             int v1, uint32_t* cells, int* s_id, float* s_val, int* s_count, int bad) {
   using C = CellOf<BITS>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int nv = v1 - v0;
   const bool counted = r.len > 0;
   const bool biased = r.bias_end > r.bias_begin;
+  int listed = 0;  // biases of the slice
 
   // ---- cells and the slice's biases
+  // The first round of the row's biases sets out too.
+  int id = -1;
+  float val = 0.0f;
+  if (r.bias_begin + tid < r.bias_end)
+    id = P.bias_ids[r.bias_begin + tid], val = P.bias_values[r.bias_begin + tid];
   if (counted) {
     const int words = (nv * (BITS / 8) + 15) / 16;
     for (int i = tid; i < words; i += kThreads)
       reinterpret_cast<uint4*>(cells)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    auto note = [&](int tok, int at) {
+    auto one = [&](int tok, bool made) {
       const uint32_t i = static_cast<uint32_t>(tok - v0);
       if (i >= static_cast<uint32_t>(nv)) return;
-      if (at >= r.prompt) cell_add<BITS>(cells, i, 1u);
+      if (made) cell_add<BITS>(cells, i, 1u);
       else cell_or<BITS>(cells, i, C::kSeen);
     };
-    // 16-byte loads from the first aligned entry on.
+    auto note = [&](int tok, int at) { one(tok, at >= r.prompt); };
+    // 16-byte loads from the first aligned entry on; nearly every four lie on
+    // one side of the prompt's end.
     const int head = min(
         r.len, static_cast<int>((4 - ((reinterpret_cast<uintptr_t>(r.hist) >> 2) & 3)) & 3));
     const int quads = (r.len - head) >> 2;
     if (tid < head) note(r.hist[tid], tid);
     const int4* h4 = reinterpret_cast<const int4*>(r.hist + head);
-#pragma unroll 4
+#pragma unroll 2
     for (int i = tid; i < quads; i += kThreads) {
       const int4 t = h4[i];
       const int at = head + 4 * i;
-      note(t.x, at), note(t.y, at + 1), note(t.z, at + 2), note(t.w, at + 3);
+      if (at >= r.prompt) {
+        one(t.x, true), one(t.y, true), one(t.z, true), one(t.w, true);
+      } else if (at + 3 < r.prompt) {
+        one(t.x, false), one(t.y, false), one(t.z, false), one(t.w, false);
+      } else {
+        note(t.x, at), note(t.y, at + 1), note(t.z, at + 2), note(t.w, at + 3);
+      }
     }
     const int rest = head + 4 * quads + tid;
     if (rest < r.len) note(r.hist[rest], rest);
   }
-  if (biased && tid >= kThreads - 32) {
-    // The last warp gathers the slice's biases in list order.
+  if (biased) {
+    // The slice's biases in list order, a thread an entry and round.
     int n = 0;
-    for (int e0 = r.bias_begin; e0 < r.bias_end; e0 += 32) {
-      const int e = e0 + lane;
-      int id = -1;
-      if (e < r.bias_end) id = P.bias_ids[e];
+    for (int e0 = r.bias_begin; e0 < r.bias_end; e0 += kThreads) {
+      const int e = e0 + tid;
+      if (e0 != r.bias_begin) {
+        id = -1;
+        if (e < r.bias_end) id = P.bias_ids[e], val = P.bias_values[e];
+      }
+      if (e < r.bias_end && (id < 0 || id >= P.V)) bad |= PKV_ST_COL_OOB;
       const bool mine = id >= v0 && id < v1;
       const unsigned m = __ballot_sync(kFull, mine);
-      const int at = n + __popc(m & ((1u << lane) - 1u));
-      if (mine && at < kBiasCap) s_id[at] = id, s_val[at] = P.bias_values[e];
-      n += __popc(m);
+      if (e0 != r.bias_begin) __syncthreads();  // the counts have been read
+      if (lane == 0) s_count[tid >> 5] = __popc(m);
+      __syncthreads();
+      int at = n + __popc(m & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int c = s_count[w];
+        if (w < (tid >> 5)) at += c;
+        n += c;
+      }
+      if (mine && at < kBiasCap) s_id[at] = id, s_val[at] = val;
     }
-    if (lane == 0) *s_count = n;
+    listed = n;
+    if (tid < 4 && n + tid < kBiasCap) s_id[n + tid] = -1;  // the last four's rest
   }
   __syncthreads();
 
-  // Calls f(token, sum of x and its biases) in the thread of each biased
-  // token's first bias.
-  auto each_biased = [&](auto&& f) {
-    const int n = *s_count;
-    const bool gathered = n <= kBiasCap;
-    const int* ids = gathered ? s_id : P.bias_ids;
-    const float* vals = gathered ? s_val : P.bias_values;
-    const int e0 = gathered ? 0 : r.bias_begin, e1 = gathered ? n : r.bias_end;
-    for (int e = e0 + tid; e < e1; e += kThreads) {
-      const int id = ids[e];
-      if (id < v0 || id >= v1) continue;
+  if (v0 == 0 && bad != 0 && P.status != nullptr) atomicOr(P.status, bad);
+
+  // The thread of a biased token's first bias has the token, and its logit with
+  // all its biases: `mine` is the token or -1.  A slice's gathered list has at
+  // most an entry a thread; a longer one is not gathered, and searched in place.
+  auto penalty = [&](int v, float x) {
+    if (!counted) return x;
+    return penalise<BITS>(
+        r, x, INPLACE ? cell_take<BITS>(cells, v - v0) : cell_get<BITS>(cells, v - v0));
+  };
+  const T* src = INPLACE ? out : in;
+  int mine = -1;
+  float mine_x = 0.0f;
+  if (listed <= kBiasCap && tid < listed) {
+    mine = s_id[tid];
+    mine_x = load_one(src + mine);
+    int before = 0, same = 0;
+    for (int k = 0; k < listed; k += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(s_id + k);
+      const int m = (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+      same += m;
+      if (k + 3 < tid) before += m;
+    }
+    for (int k = tid & ~3; k < tid; ++k) before += s_id[k] == mine;
+    if (before != 0) {
+      mine = -1;
+    } else {
+      mine_x = penalty(mine, mine_x);
+      if (same == 1) mine_x += s_val[tid];
+      else
+        for (int k = tid; k < listed; ++k)
+          if (s_id[k] == mine) mine_x += s_val[k];
+      if (!allowed(r, mine)) mine = -1;
+    }
+  }
+  auto store_biased = [&] {
+    if (mine >= 0) store_one(out + mine, mine_x);
+    if (listed <= kBiasCap) return;
+    for (int e = r.bias_begin + tid; e < r.bias_end; e += kThreads) {
+      const int v = P.bias_ids[e];
+      if (v < v0 || v >= v1) continue;
       bool first = true;
-      for (int k = e0; k < e && first; ++k) first = ids[k] != id;
+      for (int k = r.bias_begin; k < e && first; ++k) first = P.bias_ids[k] != v;
       if (!first) continue;
-      f(id, [&](float x) {
-        for (int k = e; k < e1; ++k)
-          if (ids[k] == id) x += vals[k];
-        return x;
-      });
+      float x = penalty(v, load_one(src + v));
+      for (int k = e; k < r.bias_end; ++k)
+        if (P.bias_ids[k] == v) x += P.bias_values[k];
+      if (allowed(r, v)) store_one(out + v, x);
     }
   };
 
   if (INPLACE) {
     if (biased) {
-      each_biased([&](int v, auto&& add) {
-        const uint32_t c = counted ? cell_take<BITS>(cells, v - v0) : 0u;
-        store_one(out + v, add(penalise<BITS>(r, load_one(out + v), c)));
-      });
+      store_biased();
       __syncthreads();
     }
     for (int i = tid; i < r.len; i += kThreads) {
@@ -251,22 +317,37 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
       uint32_t cw[kWords];
       uint32_t any = 0u;
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) cw[k] = counted ? cells[at * BITS / 32 + k] : 0u;
+      for (int k = 0; k < kWords; k += kWords < 4 ? 2 : 4) {
+        if (kWords < 4) {
+          uint2 c = make_uint2(0u, 0u);
+          if (counted) c = *reinterpret_cast<const uint2*>(cells + at * BITS / 32);
+          cw[k] = c.x, cw[k + 1] = c.y;
+        } else {
+          uint4 c = make_uint4(0u, 0u, 0u, 0u);
+          if (counted) c = *reinterpret_cast<const uint4*>(cells + at * BITS / 32 + k);
+          cw[k] = c.x, cw[k + 1] = c.y, cw[k + 2] = c.z, cw[k + 3] = c.w;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kWords; ++k) any |= cw[k];
       uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
       if (any != 0u) {
+        auto cell = [&](int k) {
+          return BITS == 32 ? cw[k] : (cw[k >> 1] >> ((k & 1) * 16)) & 0xffffu;
+        };
+        if (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-          const uint32_t c = BITS == 32 ? cw[k] : (cw[k >> 1] >> ((k & 1) * 16)) & 0xffffu;
-          if (c == 0u) continue;
-          if (sizeof(T) == 4) {
-            w[k & 3] = __float_as_uint(penalise<BITS>(r, __uint_as_float(w[k & 3]), c));
-          } else {
-            const int sh = (k & 1) * 16;
-            const float x = __uint_as_float((w[(k >> 1) & 3] >> sh) << 16);
-            const uint32_t y = __bfloat16_as_ushort(__float2bfloat16_rn(penalise<BITS>(r, x, c)));
-            w[(k >> 1) & 3] = (w[(k >> 1) & 3] & ~(0xffffu << sh)) | (y << sh);
+          for (int k = 0; k < 4; ++k)
+            w[k] = __float_as_uint(penalise<BITS>(r, __uint_as_float(w[k]), cell(k)));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = cell(2 * k & (kVec - 1)), hi = cell((2 * k + 1) & (kVec - 1));
+            if ((lo | hi) == 0u) continue;
+            const float x = penalise<BITS>(r, __uint_as_float(w[k] << 16), lo);
+            const float y = penalise<BITS>(r, __uint_as_float(w[k] & 0xffff0000u), hi);
+            w[k] = __bfloat16_as_ushort(__float2bfloat16_rn(x)) |
+                   static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(y))) << 16;
           }
         }
       }
@@ -297,19 +378,16 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
   }
   if (biased) {
     __syncthreads();  // biased tokens are written over
-    each_biased([&](int v, auto&& add) {
-      const uint32_t c = counted ? cell_get<BITS>(cells, v - v0) : 0u;
-      if (allowed(r, v)) store_one(out + v, add(penalise<BITS>(r, load_one(in + v), c)));
-    });
+    store_biased();
   }
 }
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(kThreads, 2) adjust_kernel(const AdjustParams P) {
+__global__ void __launch_bounds__(kThreads, 3) adjust_kernel(const AdjustParams P) {
   extern __shared__ __align__(16) uint32_t cells[];
-  __shared__ int s_id[kBiasCap];
+  __shared__ __align__(16) int s_id[kBiasCap];
   __shared__ float s_val[kBiasCap];
-  __shared__ int s_count;
+  __shared__ int s_count[kThreads / 32];
   const int b = blockIdx.x / P.slices, sl = blockIdx.x - b * P.slices;
   const int v0 = sl * P.slice, v1 = min(P.V, v0 + P.slice);
   const T* in = static_cast<const T*>(P.logits) + b * P.in_stride;
@@ -318,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_kernel(const AdjustParams 
   Row r;
   r.mask = P.mask != nullptr ? P.mask + b * P.mask_stride : nullptr;
   r.rep = P.repetition != nullptr ? P.repetition[b] : 1.0f;
+  r.inv = 1.0f / r.rep;
   r.pres = P.presence != nullptr ? P.presence[b] : 0.0f;
   r.freq = P.frequency != nullptr ? P.frequency[b] : 0.0f;
   r.len = r.prompt = 0;
@@ -342,21 +421,14 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_kernel(const AdjustParams 
     if (e0 < 0 || e1 < e0 || e1 > P.n_bias) bad |= PKV_ST_COL_OOB;
     else r.bias_begin = e0, r.bias_end = e1;
   }
-  if (sl == 0 && P.status != nullptr) {
-    for (int e = r.bias_begin + threadIdx.x; e < r.bias_end; e += kThreads) {
-      const int v = P.bias_ids[e];
-      if (v < 0 || v >= P.V) bad |= PKV_ST_COL_OOB;
-    }
-    if (bad != 0) atomicOr(P.status, bad);
-  }
   if (r.len - r.prompt <= kMaxCount16) {
-    adjust_range<T, 16, INPLACE>(P, r, in, out, v0, v1, cells, s_id, s_val, &s_count);
+    adjust_range<T, 16, INPLACE>(P, r, in, out, v0, v1, cells, s_id, s_val, s_count, bad);
   } else {
     const int mid = min(v1, v0 + P.slice / 2);
-    adjust_range<T, 32, INPLACE>(P, r, in, out, v0, mid, cells, s_id, s_val, &s_count);
+    adjust_range<T, 32, INPLACE>(P, r, in, out, v0, mid, cells, s_id, s_val, s_count, bad);
     __syncthreads();
     if (mid < v1)
-      adjust_range<T, 32, INPLACE>(P, r, in, out, mid, v1, cells, s_id, s_val, &s_count);
+      adjust_range<T, 32, INPLACE>(P, r, in, out, mid, v1, cells, s_id, s_val, s_count, bad);
   }
 }
 
