@@ -95,6 +95,26 @@ def test_long_histories_use_wide_counts(inplace):
     check(out, logits, p)
 
 
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("spread", [20, 5000, 70000])
+@pytest.mark.parametrize("many", [512, 513, 3000])
+def test_long_bias_lists(many, spread, inplace):
+    """More biases than a slice gathers, in one slice and over several, with repeats."""
+    logits, p = problem(2, 70000, 50, 3, 45, torch.float32)
+    g = torch.Generator().manual_seed(46)
+    p["bias_ptr"] = torch.tensor([0, 2, 2 + many], dtype=torch.int32)
+    p["bias_ids"] = torch.randint(0, spread, (2 + many,), generator=g).to(torch.int32)
+    p["bias_values"] = torch.randn(2 + many, generator=g)
+    x = logits.to(DEV)
+    out = pkv.adjust_logits(x, out=None if inplace else torch.empty_like(x), **dev(p)).cpu().double()
+    want, size = ref.adjust(logits, **p)
+    hidden = want == -math.inf
+    assert torch.equal(out == -math.inf, hidden)
+    # A rounding for each addend of a token, and a few before them.
+    most = int(torch.bincount(p["bias_ids"].long()).max())
+    assert bool(((out - want).abs() <= (most + 8) * 2.0 ** -24 * size)[~hidden].all())
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 def test_strides_that_are_not_aligned(dt):
     logits, p = problem(4, 2050, 100, 20, 43, dt)
