@@ -19,7 +19,7 @@ size_t workspace_need(int max_q_len, int group, int head_dim) {
   size_t partials =
       pkv::row_partial_bytes(pkv::row_block(max_q_len, group), pkv::row_ctas(sms), head_dim);
   if (pkv::has_tiles(max_q_len, group))
-    partials = std::max(partials, pkv::tile_partial_bytes(pkv::tile_ctas(sms), head_dim));
+    partials += pkv::tile_partial_bytes(pkv::tile_ctas(sms), head_dim);
   return pkv::counter_bytes(sms) + partials;
 }
 
@@ -98,19 +98,27 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   P.max_q_len = max_q_len;
   P.q_heads = q_heads;
   P.group = group;
+  P.group_div = Divider::by(static_cast<uint32_t>(group));
   P.window = std::max(window, 0);
   P.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   P.bf16 = dt == PKV_BF16;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int sms = num_sms();
   uint32_t* counters = static_cast<uint32_t*>(workspace);
-  P.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(sms));
-  P.counters = counters;
-  cudaError_t e = launch_attend_rows(P, row_block(max_q_len, group), row_ctas(sms), st);
-  if (e == cudaSuccess && has_tiles(max_q_len, group)) {
+  float* partials =
+      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(sms));
+  const bool tiles = has_tiles(max_q_len, group);
+  cudaError_t e = cudaSuccess;
+  if (tiles) {
     P.counters = counters + row_counters(sms);
+    P.partials = partials + row_partial_bytes(row_block(max_q_len, group), row_ctas(sms),
+                                              cache->head_dim) / 4;
     e = launch_attend_tiles(P, tile_ctas(sms), st);
   }
+  P.counters = counters;
+  P.partials = partials;
+  if (e == cudaSuccess)
+    e = launch_attend_rows(P, row_block(max_q_len, group), row_ctas(sms), tiles, st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();
 }

@@ -32,6 +32,7 @@ struct Divider {
 struct AttendParams {
   pkv_kv_cache c;
   Divider page_div;            // by c.page_size
+  Divider group_div;           // by group
   uint32_t page_step, token_step, head_step;  // c's strides in 16 bytes
   const uint16_t* q;
   uint16_t* out;
@@ -63,8 +64,8 @@ inline bool has_tiles(int max_q_len, int group) {
 
 // The workspace begins with both kernels' counters, at places that depend on
 // the device alone, so that calls of any shape can follow one another on it.
-// The partial results come after; the kernels run one after the other and use
-// the same bytes for theirs.
+// The partial results come after, the row kernel's first: the kernels run side
+// by side.
 constexpr int kRowCtasPerSm = 3, kRowWarps = 4;
 inline int row_ctas(int num_sms) { return num_sms * kRowCtasPerSm; }
 inline int row_counters(int num_sms) { return 3 * kRowWarps * row_ctas(num_sms); }
@@ -80,7 +81,10 @@ int row_block(int max_q_len, int group);
 size_t row_partial_bytes(int rows, int ctas, int head_dim);
 size_t tile_partial_bytes(int ctas, int head_dim);
 
-cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, cudaStream_t stream);
+// beside: the launch before it on the stream is the same call's tile kernel, and
+// the two may run side by side.
+cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, bool beside,
+                               cudaStream_t stream);
 cudaError_t launch_attend_tiles(const AttendParams& P, int ctas, cudaStream_t stream);
 
 }  // namespace pkv

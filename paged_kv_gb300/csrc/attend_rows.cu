@@ -46,6 +46,8 @@ namespace {
 constexpr int kWarps = kRowWarps;
 constexpr int kStep = 32;                // positions a warp takes at a time: one a lane
 constexpr int kStages = 2;               // ring slots of a warp
+constexpr int kLeast = 2;
+constexpr int kLook = 4;
 constexpr int kGroup = 16;               // warps whose partials are joined first
 static_assert(kStep == 32, "a lane looks up one position");
 constexpr float kUnit = 8.0f;            // a weight in fp16 is this times 2^(s - m) vs
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   using L = Layout<DP>;
   constexpr int kRows = 8 * NT;
   constexpr int kChunks = DP / 16;
-  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit};
+  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit, kLeast};
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row_lane = lane >> 2, col_lane = lane & 3;
@@ -205,7 +207,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
 
   Cursor ld;  // where this warp loads
   const Range range = find_range<kWarps * 32, kWarps>(P, kShape, smem, &ld);
-  if (ld.left == 0) return;
+  if (ld.left == 0) {
+    grid_dependency_wait();
+    return;
+  }
   Cursor cu = ld;  // where it computes
 
   // Ring: columns past head_dim stay zero throughout.
@@ -224,13 +229,20 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   const int chunks = P.c.head_dim >> 4;
   int issued = 0;
 
-  // The location of this lane's position in the next unit, read a unit ahead.
-  auto look = [&]() -> int {
-    const int tok = ld.k.start + ld.tile * kStep + lane;
-    const bool in = ld.left > 0 && tok >= ld.k.lo && tok < ld.k.end;
-    return in ? P.page_table[ld.r.table_row * P.pt_cols + tok] : -1;
+  // The locations of this lane's position in the next units of the block, up to
+  // kLook of them read at once, a unit ahead.
+  int next[kLook], known = 0;
+  auto look = [&]() {
+    const int32_t* row = P.page_table + ld.r.table_row * P.pt_cols;
+    known = static_cast<int>(min(ld.left, static_cast<int64_t>(min(ld.k.tiles - ld.tile, kLook))));
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const int tok = ld.k.start + (ld.tile + i) * kStep + lane;
+      next[i] = -1;
+      if (i < known && tok >= ld.k.lo && tok < ld.k.end) next[i] = row[tok];
+    }
   };
-  int loc = look();
+  look();
   constexpr int kPer = 32 / kChunks;  // positions a round of the warp's copies covers
   const int ch = lane % kChunks;
   // Copies the next unit, or commits an empty group.
@@ -238,6 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     if (ld.left > 0) {
       const uint32_t slot = ring + (issued % kStages) * (L::kSlot + L::kScales);
       ++issued;
+      int loc = next[0];
       const bool valid = loc >= 0 && loc < slots;
       if (!valid) {
         const int tok = ld.k.start + ld.tile * kStep + lane;
@@ -271,7 +284,12 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       }
       --ld.left;
       if (++ld.tile >= ld.k.tiles && ld.left > 0) next_block(P, ld, kShape);
-      loc = look();
+      if (--known == 0) {
+        look();
+      } else {
+#pragma unroll
+        for (int i = 1; i < kLook; ++i) next[i - 1] = next[i];
+      }
     }
     cp_async_commit();
   };
@@ -658,25 +676,40 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     if (cu.left > 0) next_block(P, cu, kShape);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  grid_dependency_wait();  // this grid ends no sooner than the tile kernel's
 }
 
 template <typename T, int DP, int NT>
-cudaError_t launch(const AttendParams& P, int ctas, cudaStream_t stream) {
+cudaError_t launch(const AttendParams& P, int ctas, bool beside, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0ull};
   const auto kernel = attend_rows_kernel<T, DP, NT>;
   constexpr int bytes = Layout<DP>::kBytes;
   const cudaError_t e = set_smem_limit_once(done, kernel, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kWarps * 32, bytes, stream>>>(P);
-  return cudaGetLastError();
+  // After the tile kernel it need not wait for that, whose results are other
+  // rows': it starts wherever that leaves room.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(ctas);
+  config.blockDim = dim3(kWarps * 32);
+  config.dynamicSmemBytes = bytes;
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&config, kernel, P);
 }
 
 template <typename T>
-cudaError_t launch_type(const AttendParams& P, int rows, int ctas, cudaStream_t stream) {
+cudaError_t launch_type(const AttendParams& P, int rows, int ctas, bool beside,
+                        cudaStream_t stream) {
   const bool wide = P.c.head_dim > 64;
   if (rows == 8)
-    return wide ? launch<T, 128, 1>(P, ctas, stream) : launch<T, 64, 1>(P, ctas, stream);
-  return wide ? launch<T, 128, 2>(P, ctas, stream) : launch<T, 64, 2>(P, ctas, stream);
+    return wide ? launch<T, 128, 1>(P, ctas, beside, stream)
+                : launch<T, 64, 1>(P, ctas, beside, stream);
+  return wide ? launch<T, 128, 2>(P, ctas, beside, stream)
+              : launch<T, 64, 2>(P, ctas, beside, stream);
 }
 
 }  // namespace
@@ -689,9 +722,10 @@ size_t row_partial_bytes(int rows, int ctas, int head_dim) {
   return static_cast<size_t>(ctas) * kWarps * 2 * partial_floats(rows, head_dim > 64 ? 128 : 64) * 4;
 }
 
-cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, cudaStream_t stream) {
-  return P.bf16 ? launch_type<__nv_bfloat16>(P, rows, ctas, stream)
-                : launch_type<__half>(P, rows, ctas, stream);
+cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, bool beside,
+                               cudaStream_t stream) {
+  return P.bf16 ? launch_type<__nv_bfloat16>(P, rows, ctas, beside, stream)
+                : launch_type<__half>(P, rows, ctas, beside, stream);
 }
 
 }  // namespace pkv

@@ -64,7 +64,7 @@ constexpr int kPart = 32;                // columns a softmax thread has in regi
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kWaitTries = 1 << 20;
 __host__ __device__ constexpr UnitShape unit_shape() {
-  return UnitShape{kBlockRows, kTile, kRowLimit + 1, int64_t{1} << 40};
+  return UnitShape{kBlockRows, kTile, kRowLimit + 1, int64_t{1} << 40, 1};
 }
 
 // P and V are of the queries' type.  An entry of P is `unit` 2^(s - m) vs, and
@@ -370,6 +370,18 @@ __device__ __forceinline__ void widen(const uint4& c, uint4& lo, uint4& hi) {
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// Two fp16 values as e4m3 codes, to nearest.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Zeroes the NaN codes of a word; true if there were any.
 __device__ __forceinline__ bool drop_nans(uint32_t& w) {
   const uint32_t hit = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
@@ -559,8 +571,8 @@ __device__ __noinline__ void rescale(uint32_t o_tmem, int d, uint32_t p_tmem, in
   }
 }
 
-// The largest s + log2 vs of kPart columns of a row.
-template <bool MASK, bool GROUPS>
+// The largest s + log2 vs of kPart columns of a row, of those in [from, to].
+template <bool GROUPS>
 __device__ __noinline__ float highest(uint32_t s_tmem, const float* sc, const float4* gr, int from,
                                       int to, float factor) {
   uint32_t x[kPart];
@@ -570,21 +582,21 @@ __device__ __noinline__ float highest(uint32_t s_tmem, const float* sc, const fl
   for (int k = 0; k < kPart; ++k) {
     const float ks = GROUPS ? gr[k / 16].x : sc[k], lv = GROUPS ? gr[k / 16].y : sc[kTile + k];
     const float t = fmaf(__uint_as_float(x[k]), ks * factor, lv);
-    if (!MASK || (k >= from && k <= to)) most = fmaxf(most, t);
+    if (k >= from && k <= to) most = fmaxf(most, t);
   }
   return most;
 }
 
 // One row's softmax of one unit: reads S, adds to l, leaves P in S's place.
-// MASK: columns outside [from, to] are not seen.  GROUPS: scales are the same
-// over 16 columns.  W: P's type.
+// Columns outside [from, to] are not seen.  GROUPS: scales are the same over 16
+// columns.  W: P's type.
 //
 // S goes through the registers kPart columns at a time (all 128 would not fit).
 // The reference m is not the running maximum but one from the row's first
 // columns, for as long as the weights under it stay below W's limit; their sum
 // shows that, so no maximum is taken.  Where it is passed, m and what was
 // summed under it move, and the columns are done again.
-template <bool MASK, bool GROUPS, typename W>
+template <bool GROUPS, typename W>
 __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
                                                const float4* gr, int from, int to, float factor,
                                                int o_cols, float m, float l) {
@@ -596,7 +608,7 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
     for (;;) {
       uint32_t x[kPart];
       tc::ld32(s_tmem + kPart * q, x);
-      if (MASK) {
+      if (__any_sync(kFull, from > 0 || to < kPart - 1)) {
 #pragma unroll
         for (int k = 0; k < kPart; ++k)
           if (k < from || k > to) x[k] = 0xff800000u;
@@ -637,7 +649,7 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
       const float2 h = unpack2(held);
       const bool past = !(h.x + h.y <= Weight<W>::limit) || m == -INFINITY;
       if (moved || !__any_sync(kFull, past)) break;
-      const float most = highest<MASK, GROUPS>(s_tmem + kPart * q, sc, gr, from, to, factor);
+      const float most = highest<GROUPS>(s_tmem + kPart * q, sc, gr, from, to, factor);
       const float now = past ? fmaxf(m, most) : m;
       const float f = m == -INFINITY ? 0.0f : ex2(m - now);
       m = now;
@@ -655,11 +667,11 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
   return make_float2(m, l);
 }
 
-template <bool GROUPS, typename W>
-__device__ __noinline__ float2 softmax_masked(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
-                                              const float4* gr, int from, int to, float factor,
-                                              int o_cols, float m, float l) {
-  return softmax_unit<true, GROUPS, W>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
+template <typename W>
+__device__ __noinline__ float2 softmax_mixed(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
+                                             const float4* gr, int from, int to, float factor,
+                                             int o_cols, float m, float l) {
+  return softmax_unit<false, W>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
 }
 
 // What a block's units need of one softmax thread.
@@ -671,13 +683,12 @@ struct RowState {
 
 // The softmax of one row over `n` units.
 //   from, to: columns of the first unit that the row sees, going down by kTile
-//   a unit; all_from, all_to: those that every row of the tile sees;
-//   tile: bit 0 the tile, bit 1 scales by groups may be used.
+//   a unit;  tile: bit 0 the tile, bit 1 scales by groups may be used.
 template <typename W>
 __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float* s_sc,
                                                const float4* s_gr, uint32_t s_tmem, uint32_t o_tmem,
                                                float factor, int d, int n, int from, int to,
-                                               int all_from, int all_to, int tile) {
+                                               int tile) {
   const int t = tile & 1;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
@@ -689,21 +700,17 @@ __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float*
     const int cols = j > 0 ? d : 0;
     const int* mixed = B->mixed[slot];
     const bool groups = (tile & 2) != 0 && (mixed[0] | mixed[1] | mixed[2]) == 0;
-    float2 ml;
-    if (groups && all_from <= 0 && all_to >= kTile - 1) {
-      ml = softmax_unit<false, true, W>(s_tmem, o_tmem, s_sc, gr, 0, 0, factor, cols, r.m, r.l);
-    } else {
-      const float* sc = s_sc + slot * 3 * kTile;
-      ml = groups ? softmax_masked<true, W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
-                  : softmax_masked<false, W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
-    }
+    const float2 ml =
+        groups ? softmax_unit<true, W>(s_tmem, o_tmem, s_sc, gr, from, to, factor, cols, r.m, r.l)
+               : softmax_mixed<W>(s_tmem, o_tmem, s_sc + slot * 3 * kTile, gr, from, to, factor, cols,
+                                  r.m, r.l);
     r.m = ml.x;
     r.l = ml.y;
     tc::wait_st();
     tc::fence_before();
     arrive(&B->p_full[t]);
     ++r.unit;
-    from -= kTile, to -= kTile, all_from -= kTile, all_to -= kTile;
+    from -= kTile, to -= kTile;
   }
   return r;
 }
@@ -713,7 +720,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
                                           uint8_t* smem, Bars* B, int t) {
   using L = Plan<NS>;
   static_assert(L::kSc == Plan<2>::kSc, "one ring size");
-  const int tid = threadIdx.x & 127, warp = tid >> 5;  // tid: the row of the tile
+  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;  // tid: the row of the tile
   const int d = P.c.head_dim;
   const uint32_t lanes = B->tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const uint32_t s_tmem = lanes + t * kTile, o_tmem = s_tmem + 256;
@@ -731,90 +738,96 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       if (c.left > 0) next_block(P, c, unit_shape());
       continue;
     }
-    const int row = t * kTileRows + tid;  // of the block
-    const int tok = (c.k.row0 + row) / P.group, g = c.k.row0 + row - tok * P.group;
+    // This thread's row: its token and head.
+    const uint32_t at = static_cast<uint32_t>(c.k.row0 + t * kTileRows + tid);
+    const uint32_t tok = P.group_div.divide(at);
     const int64_t j_row = c.q_off + tok;
-    const int head = c.head * P.group + g;
-    const bool live = row < c.k.rows;
+    const int head = c.head * P.group + static_cast<int>(at - tok * P.group);
+    const bool live = t * kTileRows + tid < c.k.rows;
     const bool there = live && j_row < P.n_tokens;
-    // ---- the row's query as NS e4m3 rows
-    float factor;  // score (log2) of a product of codes
+    const uint32_t rows_there = __ballot_sync(kFull, there);
+    uint8_t* q = smem + L::q + t * NS * kQBytes;
+    // ---- the warp's queries, each as NS e4m3 rows.  They come as they are to
+    // the place of their first two codes (32 rows of 128 bytes in each: a row's
+    // first and second half) and are converted there.  A half warp has a row and
+    // a lane 8 channels of it.  The loops are rolled: this code runs once a
+    // block, and its fetch costs more than its instructions.
+    float factor = 0.0f;  // of this thread's row: score (log2) of a product of codes
+    const int half = lane >> 4, ch = lane & 15;
+    uint8_t* const half_row = q + (ch >> 3) * kQBytes;
     {
-      const uint16_t* src = P.q + j_row * P.q_ts + static_cast<int64_t>(head) * P.q_hs;
-      float amax = 0.0f;
-      if (there) {
+      const uint32_t dst = smem_addr(half_row);
+      const int64_t from = j_row * P.q_ts + static_cast<int64_t>(head) * P.q_hs;
 #pragma unroll 4
-        for (int i = 0; i < d; i += 8) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + i);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      for (int i = half; i < 32; i += 2) {
+        const int64_t off = __shfl_sync(kFull, from, i) + ch * 8;
+        const bool mine = ((rows_there >> i) & 1u) != 0u && ch * 8 < d;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(dst + chunk_at(warp * 32 + i, ch & 7)), "l"(P.q + (mine ? off : 0)),
+                     "r"(mine ? 16 : 0) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      const bool store = ch * 8 < ((d + 31) & ~31);  // (zeros past d: Q K^T sums over 32s)
+      const float sign = P.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll 2
+      for (int i = 0; i < 16; ++i) {
+        const int row = warp * 32 + 2 * i + half;
+        const uint4 raw = *reinterpret_cast<const uint4*>(half_row + chunk_at(row, ch & 7));
+        uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+        // The row's largest, as bits, so that a NaN is larger than all.
+        uint32_t top = 0u;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 y = Pair<T>::unpack(w[k]);
-            amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+        for (int n = 0; n < 4; ++n) top = __vmaxu2(top, x[n] & 0x7fff7fffu);
+        top = __reduce_max_sync(0xffffu << (lane & 16), max(top & 0xffffu, top >> 16));
+        const uint32_t amax = __float_as_uint(Pair<T>::unpack(top).x);
+        // To [128, 256) by a power of two.
+        const int e = static_cast<int>(amax >> 23);
+        const float unit =
+            e > 8 && e < 255 ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 1.0f;
+        const float f = __shfl_sync(kFull, unit, (lane & 1) * 16);  // (and all have read)
+        if ((lane >> 1) == i) factor = f;
+        // In fp16, whose 11 bits hold an element of either type and what is
+        // left of it after each code exactly (down to 2^-24, and the codes end
+        // at 2^-9).
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float2 z = Pair<T>::unpack(x[n]);
+          x[n] = Pair<__half>::pack(z.x * (unit * sign), z.y * (unit * sign));
+        }
+        if (store) {
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            uint32_t o[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              o[n] = e4m3x2_of_f16x2(x[n]);
+              if (s + 1 < NS) x[n] = sub_f16x2(x[n], e4m3x2_to_f16x2(o[n]));
+            }
+            // The codes have no infinity: a row that is not finite is NaNs.
+            const uint32_t a = e == 255 ? 0x7f7f7f7fu : o[0] | (o[1] << 16);
+            const uint32_t b = e == 255 ? 0x7f7f7f7fu : o[2] | (o[3] << 16);
+            *reinterpret_cast<uint2*>(q + s * kQBytes + chunk_at(row, ch >> 1) + (ch & 1) * 8) =
+                make_uint2(a, b);
           }
         }
       }
-      // To [128, 256) by a power of two.  A row that is not finite is a NaN
-      // below whatever its unit.
-      const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-      const float unit =
-          e > 8 && e < 255 ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 1.0f;
-      factor = fmaxf(fabsf(P.scale_log2) / unit, 1.17549435e-38f);  // -inf stays -inf
-      const float sign = P.scale_log2 < 0.0f ? -unit : unit;
-      uint8_t* q = smem + L::q + t * NS * kQBytes;
-#pragma unroll 1
-      for (int i = 0; i < d; i += 16) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-        if (there) {
-          x = *reinterpret_cast<const uint4*>(src + i);
-          y = *reinterpret_cast<const uint4*>(src + i + 8);
-        }
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 z = Pair<T>::unpack(w[k]);
-          v[2 * k] = z.x * sign;
-          v[2 * k + 1] = z.y * sign;
-          // The codes have no infinity.
-          if (!isfinite(v[2 * k])) v[2 * k] = __uint_as_float(0x7fffffffu);
-          if (!isfinite(v[2 * k + 1])) v[2 * k + 1] = __uint_as_float(0x7fffffffu);
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = e4m3x2(v[4 * k], v[4 * k + 1]), b = e4m3x2(v[4 * k + 2], v[4 * k + 3]);
-            o[k] = a | (b << 16);
-            const float2 ra = Pair<__half>::unpack(e4m3x2_to_f16x2(a));
-            const float2 rb = Pair<__half>::unpack(e4m3x2_to_f16x2(b));
-            v[4 * k] -= ra.x, v[4 * k + 1] -= ra.y, v[4 * k + 2] -= rb.x, v[4 * k + 3] -= rb.y;
-          }
-          *reinterpret_cast<uint4*>(q + s * kQBytes + chunk_at(tid, i >> 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
+      factor = fmaxf(fabsf(P.scale_log2) / factor, 1.17549435e-38f);  // -inf stays -inf
       tc::fence_smem();
       tc::fence_before();
       arrive(&B->q_full[t]);
     }
-    // Positions that this row sees, and those that all rows of the tile see.
-    const int pos = c.r.cached + tok;
-    int lo = c.r.begin;
+    // The positions that this thread's row sees.
+    const int pos = c.r.cached + static_cast<int>(tok);
+    int lo = c.r.begin, hi = min(pos, c.k.end - 1);
     if (P.window > 0) lo = max(lo, pos - P.window + 1);
-    const int hi = min(pos, c.k.end - 1);
+    if (!live) lo = 0, hi = INT32_MAX;  // (never without an m)
     {
-      const int first_row = c.k.row0 + t * kTileRows;
-      const int last_row = c.k.row0 + min(c.k.rows, (t + 1) * kTileRows) - 1;
-      const int all_hi = min(c.r.cached + first_row / P.group, c.k.end - 1);
-      int all_lo = c.r.begin;
-      if (P.window > 0) all_lo = max(all_lo, c.r.cached + last_row / P.group - P.window + 1);
       const int base = c.k.start + t_begin * kTile;
       st.m = -INFINITY;
       st.l = 0.0f;
       st = softmax_units<T>(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
-                         all_lo - base, all_hi - base, tile);
+                            tile);
     }
     // ---- the block's end: O is complete
     wait(B, &B->s_full[t], st.s_phase);
@@ -822,7 +835,6 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
     tc::fence_after();
     const float m = st.m, l = st.l;
     bool nan = *reinterpret_cast<volatile int*>(&B->nan) != 0;
-    const int64_t out_at = j_row * P.o_ts + static_cast<int64_t>(head) * P.o_hs;
     // NaN codes of partly seen units were left out of the products.
     auto put_nans = [&](int k, float (&o)[16]) {
       for (int p = lo; p <= hi && p < c.k.end; ++p) {
@@ -837,13 +849,28 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
           if ((v[i] & 0x7f) == 0x7f) o[i] = __uint_as_float(0x7fffffffu);
       }
     };
-    auto store16 = [&](int k, const float (&o)[16], float inv) {
+    // Results go out by way of the queries' place, which is free: rows of 2 D
+    // bytes, their first half in the first codes' rows of this warp and the
+    // second in the second's.
+    auto stage16 = [&](int k, const float (&o)[16], float inv) {
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = Pair<T>::pack(o[2 * i] * inv, o[2 * i + 1] * inv);
-      uint4* dst = reinterpret_cast<uint4*>(P.out + out_at + k);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      uint8_t* dst = q + (k >> 6) * kQBytes;
+      const int chunk = (k >> 3) & 7;
+      *reinterpret_cast<uint4*>(dst + chunk_at(tid, chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + chunk_at(tid, chunk + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+    };
+    auto store_rows = [&] {
+      __syncwarp();
+      const int64_t to = j_row * P.o_ts + static_cast<int64_t>(head) * P.o_hs;
+#pragma unroll 4
+      for (int i = half; i < 32; i += 2) {
+        const int64_t off = __shfl_sync(kFull, to, i) + ch * 8;
+        if (((rows_there >> i) & 1u) != 0u && ch * 8 < d)
+          *reinterpret_cast<uint4*>(P.out + off) =
+              *reinterpret_cast<const uint4*>(half_row + chunk_at(warp * 32 + i, ch & 7));
+      }
     };
     auto store_lse = [&](float mm, float ll) {
       if (P.lse != nullptr)
@@ -859,11 +886,10 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         float o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = l != 0.0f ? __uint_as_float(r[i]) : 0.0f;
-        if (there) {
-          if (nan) put_nans(k, o);
-          store16(k, o, inv);
-        }
+        if (there && nan) put_nans(k, o);
+        stage16(k, o, inv);
       }
+      store_rows();
       if (there) store_lse(m, l);
     } else {
       int64_t c0, c1;
@@ -897,51 +923,58 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         *reinterpret_cast<volatile int*>(&B->last[t]) = is_last ? 1 : 0;
       }
       tile_sync(t);
-      if (*reinterpret_cast<volatile int*>(&B->last[t]) != 0 && there) {
+      if (*reinterpret_cast<volatile int*>(&B->last[t]) != 0) {
         // Joined in CTA order.
         auto stat_of = [&](int64_t cta, int i) {
           return __ldcg(
               reinterpret_cast<const float2*>(partial(cta) + static_cast<int64_t>(kTileRows) * d) + i);
         };
         float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
+#pragma unroll 2
         for (int64_t cta = c0; cta <= c1; ++cta) {
           mm = fmaxf(mm, stat_of(cta, tid).x);
           nan = nan || stat_of(cta, kTileRows).x != 0.0f;
         }
         const float ref = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll 4
+#pragma unroll 2
         for (int64_t cta = c0; cta <= c1; ++cta) {
           const float2 s = stat_of(cta, tid);
           ll += s.y * ex2(s.x - ref);
         }
         const float inv = ll != 0.0f ? (1.0f / Weight<T>::unit) / ll : 0.0f;
 #pragma unroll 1
-        for (int k = 0; k < d; k += 16) {
-          float o[16];
+        for (int k = 0; k < d; k += 32) {
+          float o[2][16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+          for (int i = 0; i < 32; ++i) o[i >> 4][i & 15] = 0.0f;
 #pragma unroll 2
           for (int64_t cta = c0; cta <= c1; ++cta) {
             const float2 s = stat_of(cta, tid);
             const float f = ex2(s.x - ref);
             const float4* p = reinterpret_cast<const float4*>(partial(cta)) + (k / 4) * kTileRows + tid;
-            float4 x[4];
+            float4 x[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = __ldcg(p + i * kTileRows);
+            for (int i = 0; i < 8; ++i)
+              x[i] = k + 4 * i < d ? __ldcg(p + i * kTileRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (s.y == 0.0f) continue;  // that part saw nothing
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[4 * i] = fmaf(x[i].x, f, o[4 * i]);
-              o[4 * i + 1] = fmaf(x[i].y, f, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(x[i].z, f, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(x[i].w, f, o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) {
+              float* to = &o[i >> 2][4 * (i & 3)];
+              to[0] = fmaf(x[i].x, f, to[0]);
+              to[1] = fmaf(x[i].y, f, to[1]);
+              to[2] = fmaf(x[i].z, f, to[2]);
+              to[3] = fmaf(x[i].w, f, to[3]);
             }
           }
-          if (nan) put_nans(k, o);
-          store16(k, o, inv);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (k + 16 * i >= d) break;
+            if (nan && there) put_nans(k + 16 * i, o[i]);
+            stage16(k + 16 * i, o[i], inv);
+          }
         }
-        store_lse(mm, ll);
+        store_rows();
+        if (there) store_lse(mm, ll);
       }
     }
     __syncwarp();
@@ -957,6 +990,7 @@ template <typename T, int NS>
 __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
     const __grid_constant__ AttendParams P) {
   using L = Plan<NS>;
+  launch_dependents();  // the row kernel's blocks may start beside these
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
   Bars* B = reinterpret_cast<Bars*>(smem + L::bar);

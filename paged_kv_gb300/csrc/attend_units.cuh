@@ -17,9 +17,20 @@
 
 namespace pkv {
 
+// The row kernel runs beside the tile kernel of its call: the first's blocks
+// start when all of the second's have, wherever those leave room, and it ends
+// only when the second has.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 struct UnitShape {
   int rows, tile;
   int64_t min_rows, max_rows;
+  int least;  // units of a worker, where there are so many
 };
 
 // What the call asks of one request.
@@ -169,7 +180,7 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
   __syncthreads();
   Range g;
   g.total = total;
-  g.workers = min(static_cast<long long>(gridDim.x) * WORKERS, total);
+  g.workers = min(static_cast<long long>(gridDim.x) * WORKERS, (total + u.least - 1) / u.least);
   g.last = total;
   c->left = 0;
   const long long me = static_cast<long long>(blockIdx.x) * WORKERS + (WORKERS == 1 ? 0 : warp);
