@@ -46,8 +46,12 @@ namespace {
 constexpr int kWarps = kRowWarps;
 constexpr int kStep = 32;                // positions a warp takes at a time: one a lane
 constexpr int kStages = 2;               // ring slots of a warp
-constexpr int kLeast = 2;
-constexpr int kLook = 4;
+constexpr int kLook = 4;                 // units whose places are read at once
+// Cost of a block's start in units, and the least cost of a warp's range.  256
+// requests decoding: 149 us without the first, 135, 132 and 133 with 1, 2 and 3;
+// draft verification 35, 34, 32 and 32.  A few short requests beside a prompt
+// batch: 272 us from 1 on, 257 from 2 on (fewer partials to join).
+constexpr int kLead = 3, kLeast = 2;
 constexpr int kGroup = 16;               // warps whose partials are joined first
 static_assert(kStep == 32, "a lane looks up one position");
 constexpr float kUnit = 8.0f;            // a weight in fp16 is this times 2^(s - m) vs
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   using L = Layout<DP>;
   constexpr int kRows = 8 * NT;
   constexpr int kChunks = DP / 16;
-  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit, kLeast};
+  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit, kLeast, kLead};
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row_lane = lane >> 2, col_lane = lane & 3;
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
         }
       }
       int64_t c0, c1;
-      block_workers(range, range.last - cu.left - t_begin, cu.k.tiles, &c0, &c1);
+      block_workers(range, cu, &c0, &c1);
       // This warp's group of the block: workers [g0, g1].
       const int64_t first_group = c0 / kGroup, group = worker / kGroup;
       const int groups = static_cast<int>(c1 / kGroup - first_group) + 1;

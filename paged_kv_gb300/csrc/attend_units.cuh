@@ -3,9 +3,12 @@
 // The query rows of one (request, cache head) -- row = query token * group +
 // query head in the group -- are cut into blocks of `rows`, the positions that
 // a block sees into tiles of `tile`.  A unit is one tile of one block; a call's
-// units are ordered by request, head, block, tile, and every worker takes an
-// equal contiguous range of them (a CTA, or a warp).  A kernel takes only the requests whose row
-// count lies in [min_rows, max_rows]; others are another kernel's.
+// units are ordered by request, head, block, tile, and every worker (a CTA, or a
+// warp) takes a contiguous range of them.  The ranges cost the same, where a
+// unit costs one and the start of a block `lead` (its queries come, its results
+// leave): many short blocks are as much work as one long one of more units.  A
+// kernel takes only the requests whose row count lies in [min_rows, max_rows];
+// others are another kernel's.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -30,7 +33,8 @@ __device__ __forceinline__ void grid_dependency_wait() {
 struct UnitShape {
   int rows, tile;
   int64_t min_rows, max_rows;
-  int least;  // units of a worker, where there are so many
+  int least;  // cost of a worker's range, where there is so much
+  int lead;
 };
 
 // What the call asks of one request.
@@ -92,12 +96,12 @@ __device__ __forceinline__ int block_count(const AttendParams& P, const Request&
   return static_cast<int>((n + u.rows - 1) / u.rows);
 }
 
-__device__ __forceinline__ int64_t request_units(const AttendParams& P, const Request& r,
+__device__ __forceinline__ int64_t request_cost(const AttendParams& P, const Request& r,
                                                  const UnitShape& u) {
   const int nb = block_count(P, r, u);
-  int64_t tiles = 0;
-  for (int b = 0; b < nb; ++b) tiles += make_block(P, r, b, u).tiles;
-  return tiles * P.c.kv_heads;
+  int64_t cost = static_cast<int64_t>(nb) * u.lead;
+  for (int b = 0; b < nb; ++b) cost += make_block(P, r, b, u).tiles;
+  return cost * P.c.kv_heads;
 }
 
 // A place in the call's units: what a warp loads from or computes on.
@@ -105,13 +109,15 @@ struct Cursor {
   Request r;
   Block k;
   int64_t q_off;   // the request's first packed token
-  int64_t left;    // units left in this CTA's range
+  int64_t left;    // units left in this worker's range
+  int64_t cost;    // of everything before the block's first unit
   int req, head, block, tile;
 };
 
 // Goes to the next block.  Only called while units are left.
 __device__ __forceinline__ void next_block(const AttendParams& P, Cursor& c, const UnitShape& u) {
   c.tile = 0;
+  c.cost += c.k.tiles + u.lead;
   if (++c.block >= block_count(P, c.r, u)) {
     c.block = 0;
     if (++c.head >= P.c.kv_heads) {
@@ -129,9 +135,8 @@ __device__ __forceinline__ void next_block(const AttendParams& P, Cursor& c, con
 
 // A worker's (CTA's or warp's) range of the call's units.
 struct Range {
-  int64_t total;    // the call's units
-  int64_t workers;  // workers that have any
-  int64_t last;     // one past this worker's last unit
+  int64_t total;    // the call's cost
+  int64_t workers;  // workers that it is cut for
 };
 
 // Finds this worker's range and sets *c to its first unit (c->left 0: none).
@@ -143,7 +148,7 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
   constexpr int kW = THREADS / 32;
   static_assert(WORKERS == 1 || WORKERS == kW, "a CTA's workers");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // Units and tokens before each thread's requests.
+  // Cost and tokens before each thread's requests.
   long long* s_u = static_cast<long long*>(scratch);
   long long* s_t = s_u + THREADS;
   const int per = (P.B + THREADS - 1) / THREADS;
@@ -153,7 +158,7 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
   for (int i = i0; i < i1; ++i) {
     const Request r = load_request(P, i);
     bad |= r.bad;
-    units += request_units(P, r, u);
+    units += request_cost(P, r, u);
     toks += r.q_len;
   }
   long long ui = units, ti = toks;
@@ -181,12 +186,11 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
   Range g;
   g.total = total;
   g.workers = min(static_cast<long long>(gridDim.x) * WORKERS, (total + u.least - 1) / u.least);
-  g.last = total;
   c->left = 0;
   const long long me = static_cast<long long>(blockIdx.x) * WORKERS + (WORKERS == 1 ? 0 : warp);
   if (me < g.workers) {
     const long long first = me * total / g.workers;
-    g.last = (me + 1) * total / g.workers;
+    const long long last = (me + 1) * total / g.workers;
     // The last thread whose requests begin at or before `first` (threads
     // without units begin where the next one does, and are passed over).
     int k = 0;
@@ -197,11 +201,10 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
     k = __reduce_max_sync(kFull, k);
     long long at = first - s_u[k];
     c->q_off = s_t[k];
-    c->left = g.last - first;
     c->req = k * per;
     for (;;) {
       c->r = load_request(P, c->req);
-      const long long n = request_units(P, c->r, u);
+      const long long n = request_cost(P, c->r, u);
       if (at < n) {
         const long long per_head = n / P.c.kv_heads;
         c->head = static_cast<int>(at / per_head);
@@ -215,21 +218,32 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
     c->block = 0;
     for (;;) {
       c->k = make_block(P, c->r, c->block, u);
-      if (at < c->k.tiles) break;
-      at -= c->k.tiles;
+      if (at < c->k.tiles + u.lead) break;
+      at -= c->k.tiles + u.lead;
       ++c->block;
     }
-    c->tile = static_cast<int>(at);
+    c->cost = first - at + u.lead;
+    c->tile = max(0, static_cast<int>(at) - u.lead);
+    // The range's units.
+    Cursor n = *c;
+    long long rest = last - c->cost;
+    while (n.tile < rest) {
+      const long long here = min(static_cast<long long>(n.k.tiles), rest);
+      c->left += here - n.tile;
+      rest -= n.k.tiles + u.lead;
+      if (rest <= 0) break;
+      next_block(P, n, u);
+    }
   }
   __syncthreads();
   return g;
 }
 
-// The workers that hold a block's first and last unit, given its first unit.
-__device__ __forceinline__ void block_workers(const Range& g, int64_t block_first, int tiles,
-                                              int64_t* c0, int64_t* c1) {
-  *c0 = ((block_first + 1) * g.workers - 1) / g.total;
-  *c1 = ((block_first + tiles) * g.workers - 1) / g.total;
+// The workers that hold the first and the last unit of the cursor's block.
+__device__ __forceinline__ void block_workers(const Range& g, const Cursor& c, int64_t* c0,
+                                              int64_t* c1) {
+  *c0 = ((c.cost + 1) * g.workers - 1) / g.total;
+  *c1 = ((c.cost + c.k.tiles) * g.workers - 1) / g.total;
 }
 
 }  // namespace pkv
