@@ -773,7 +773,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       __syncwarp();
       const bool store = ch * 8 < ((d + 31) & ~31);  // (zeros past d: Q K^T sums over 32s)
       const float sign = P.scale_log2 < 0.0f ? -1.0f : 1.0f;
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; i < 16; ++i) {
         const int row = warp * 32 + 2 * i + half;
         const uint4 raw = *reinterpret_cast<const uint4*>(half_row + chunk_at(row, ch & 7));
@@ -782,14 +782,17 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         uint32_t top = 0u;
 #pragma unroll
         for (int n = 0; n < 4; ++n) top = __vmaxu2(top, x[n] & 0x7fff7fffu);
-        top = __reduce_max_sync(0xffffu << (lane & 16), max(top & 0xffffu, top >> 16));
-        const uint32_t amax = __float_as_uint(Pair<T>::unpack(top).x);
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
         // To [128, 256) by a power of two.
-        const int e = static_cast<int>(amax >> 23);
+        const int e = static_cast<int>(__float_as_uint(Pair<T>::unpack(top).x) >> 23);
         const float unit =
             e > 8 && e < 255 ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 1.0f;
         const float f = __shfl_sync(kFull, unit, (lane & 1) * 16);  // (and all have read)
         if ((lane >> 1) == i) factor = f;
+        // The codes have no infinity: a row that is not finite is NaNs.
+        const uint32_t nans = e == 255 ? 0x7f7f7f7fu : 0u;
         // In fp16, whose 11 bits hold an element of either type and what is
         // left of it after each code exactly (down to 2^-24, and the codes end
         // at 2^-9).
@@ -798,21 +801,17 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
           const float2 z = Pair<T>::unpack(x[n]);
           x[n] = Pair<__half>::pack(z.x * (unit * sign), z.y * (unit * sign));
         }
-        if (store) {
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            uint32_t o[4];
+        for (int s = 0; s < NS; ++s) {
+          uint32_t o[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              o[n] = e4m3x2_of_f16x2(x[n]);
-              if (s + 1 < NS) x[n] = sub_f16x2(x[n], e4m3x2_to_f16x2(o[n]));
-            }
-            // The codes have no infinity: a row that is not finite is NaNs.
-            const uint32_t a = e == 255 ? 0x7f7f7f7fu : o[0] | (o[1] << 16);
-            const uint32_t b = e == 255 ? 0x7f7f7f7fu : o[2] | (o[3] << 16);
-            *reinterpret_cast<uint2*>(q + s * kQBytes + chunk_at(row, ch >> 1) + (ch & 1) * 8) =
-                make_uint2(a, b);
+          for (int n = 0; n < 4; ++n) {
+            o[n] = e4m3x2_of_f16x2(x[n]);
+            if (s + 1 < NS) x[n] = sub_f16x2(x[n], e4m3x2_to_f16x2(o[n]));
           }
+          if (store)
+            *reinterpret_cast<uint2*>(q + s * kQBytes + chunk_at(row, ch >> 1) + (ch & 1) * 8) =
+                make_uint2((o[0] | (o[1] << 16)) | nans, (o[2] | (o[3] << 16)) | nans);
         }
       }
       factor = fmaxf(fabsf(P.scale_log2) / factor, 1.17549435e-38f);  // -inf stays -inf
