@@ -16,7 +16,8 @@
 // thread of a token's first bias adds all of them, so the sum has one order.
 //
 // Cells are 16 bits where the row's made tokens number at most 16383 (a
-// 14-bit count), else 32 bits, in two passes of half a slice.
+// 14-bit count), else 32 bits, in two passes of half a slice.  (32 bits for all:
+// the two sizes below take 55 and 517 us, 4 x 32000 fp32 6.2 against 4.6.)
 //
 // Bound: bytes (out of place: one read and one write of the logits).  For 256 x
 // 151936 bf16 (histories to 2512 tokens, 64 biases a row, a third of the rows
@@ -519,7 +520,8 @@ extern "C" int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dty
   P.B = B, P.V = V;
   P.vec = aligned16(logits) && aligned16(out) && (row_stride * elt) % 16 == 0 &&
           (out_stride * elt) % 16 == 0;
-  // Slices: as few as the cells allow, but enough for two CTAs an SM; a
+  // Slices: as few as the cells allow, but enough for two CTAs an SM (otherwise
+  // 4 x 32000 fp32 takes 7.9 us instead of 4.6, 16 x 151936 bf16 8.7 of 6.9); a
   // multiple of 2048 tokens, so that no mask word or vector straddles two
   // (or two halves of one).
   const int cap = kCellBytes / 2;

@@ -16,8 +16,7 @@ namespace {
 
 size_t workspace_need(int max_q_len, int group, int head_dim) {
   const int sms = pkv::num_sms();
-  size_t partials =
-      pkv::row_partial_bytes(pkv::row_block(max_q_len, group), pkv::row_ctas(sms), head_dim);
+  size_t partials = pkv::row_partial_bytes(pkv::row_ctas(sms), head_dim);
   if (pkv::has_tiles(max_q_len, group))
     partials += pkv::tile_partial_bytes(pkv::tile_ctas(sms), head_dim);
   return pkv::counter_bytes(sms) + partials;
@@ -111,14 +110,13 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   cudaError_t e = cudaSuccess;
   if (tiles) {
     P.counters = counters + row_counters(sms);
-    P.partials = partials + row_partial_bytes(row_block(max_q_len, group), row_ctas(sms),
-                                              cache->head_dim) / 4;
+    P.partials = partials + row_partial_bytes(row_ctas(sms), cache->head_dim) / 4;
     e = launch_attend_tiles(P, tile_ctas(sms), st);
   }
   P.counters = counters;
   P.partials = partials;
   if (e == cudaSuccess)
-    e = launch_attend_rows(P, row_block(max_q_len, group), row_ctas(sms), tiles, st);
+    e = launch_attend_rows(P, row_ctas(sms), tiles, st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();
 }

@@ -2,9 +2,9 @@
 // (one token a request), verification of a few draft tokens.
 //
 // A row is one (query token, query head); the rows of one cache head share its
-// keys and values.  A work unit is kStep positions for one block of up to 8 * NT
+// keys and values.  A work unit is kStep positions for one block of up to kRows
 // rows of one (request, cache head).  All units of the call, in batch order,
-// are cut into equal contiguous ranges, one per warp, so ragged lengths balance
+// are cut into contiguous ranges of equal cost, one per warp, so ragged lengths balance
 // and one long request fills the machine.  A warp that holds only part of a
 // block leaves its partial (m, l, O) in the workspace; partials are joined in
 // warp order, first within groups of kGroup warps, then over the groups, each
@@ -24,7 +24,17 @@
 // where the weights under it sum to more than 2^15.  So a unit needs no maximum
 // over its lanes, and few units rescale.
 //
-// Bound: bytes.  Each cached byte is read once (2 D per position and head).
+// Bound: bytes.  Each cached byte is read once (2 D per position and head), and
+// close behind the issue of 716 instructions a unit (half of them conversions
+// of codes and their addresses).  256 requests of up to 2513 positions, 16 query
+// and 8 cache heads of 128, pages of 16, bf16: 132 us, 5.2 TB/s; 16 of up to
+// 36864, 32 and 4 heads, pages of 64, fp16: 73 us, 4.0 TB/s; 61 of up to 2006
+// under a window of 777 with 1 to 5 new tokens, 12 heads of 64, pages of 1: 32
+// us (scattered rows of 64 bytes); one of 701: 14.5 us, of which the joins 5 and
+// the rest the start's chain of loads (lengths, places, rows).
+// Blocks of 16 rows, which read the cache half as often but spill and leave one
+// row in two idle where there are 8: 256 requests of 16 rows 292 us against 258
+// (of 32: 538 against 479), 16 long ones of 16 rows 143 against 113.
 
 #include <cuda_runtime.h>
 
@@ -44,15 +54,19 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = kRowWarps;
+constexpr int kRows = 8;                 // of a block: the narrow side of the products
 constexpr int kStep = 32;                // positions a warp takes at a time: one a lane
 constexpr int kStages = 2;               // ring slots of a warp
-constexpr int kLook = 4;                 // units whose places are read at once
+constexpr int kLook = 4;                 // units whose places are read at once (1: 149 us for the
+                                         // 256 requests against 145, 8: 154)
 // Cost of a block's start in units, and the least cost of a warp's range.  256
 // requests decoding: 149 us without the first, 135, 132 and 133 with 1, 2 and 3;
 // draft verification 35, 34, 32 and 32.  A few short requests beside a prompt
 // batch: 272 us from 1 on, 257 from 2 on (fewer partials to join).
 constexpr int kLead = 3, kLeast = 2;
-constexpr int kGroup = 16;               // warps whose partials are joined first
+// Warps whose partials are joined first.  With 8, 16 and 32: one request 13.3,
+// 14.5 and 14.3 us, long contexts 72, 72 and 78.
+constexpr int kGroup = 16;
 static_assert(kStep == 32, "a lane looks up one position");
 constexpr float kUnit = 8.0f;            // a weight in fp16 is this times 2^(s - m) vs
 constexpr float kLimit = 32768.0f;       // sum of such weights that moves m
@@ -197,11 +211,10 @@ __device__ __forceinline__ void join(const AttendParams& P, int rows, int n, Slo
   }
 }
 
-template <typename T, int DP, int NT>
+template <typename T, int DP>
 __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel(
     const __grid_constant__ AttendParams P) {
   using L = Layout<DP>;
-  constexpr int kRows = 8 * NT;
   constexpr int kChunks = DP / 16;
   constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit, kLeast, kLead};
   extern __shared__ __align__(128) uint8_t smem[];
@@ -300,11 +313,11 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue();
 
-  uint32_t qf[NT][DP / 8];      // Q^T fragments
-  float cf[NT][2];              // per row: score scale in log2 units
-  int hi[NT][2], lo[NT][2];     // per row: positions seen
-  float m[NT][2], l[NT][2];
-  float o[DP / 16][NT][4];
+  uint32_t qf[DP / 8];          // Q^T fragments
+  float cf[2];                  // per row: score scale in log2 units
+  int hi[2], lo[2];             // per row: positions seen
+  float m[2], l[2];
+  float o[DP / 16][4];
   int used = 0;
 
   while (cu.left > 0) {
@@ -313,67 +326,63 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     const int t_end = static_cast<int>(min(static_cast<int64_t>(cu.k.tiles), cu.tile + cu.left));
     const bool whole = t_begin == 0 && t_end == cu.k.tiles;
     int all_hi = INT32_MAX, all_lo = 0;  // seen by every row: [all_lo, all_hi]
+    // Queries: this thread's fragment holds row row_lane,
+    // elements [col_lane * DP / 4, + DP / 4).
+    const bool live = row_lane < cu.k.rows && cu.r.end != 0;
+    const int row = cu.k.row0 + row_lane, tok = row / P.group, g = row - tok * P.group;
+    const uint16_t* src = P.q + (cu.q_off + tok) * P.q_ts +
+                          static_cast<int64_t>(cu.head * P.group + g) * P.q_hs;
+    const bool there = live && cu.q_off + tok < P.n_tokens;
+    float amax = 0.0f;
+    uint32_t raw[DP / 8];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      // Queries: this thread's fragment holds row nt * 8 + row_lane,
-      // elements [col_lane * DP / 4, + DP / 4).
-      const int row = nt * 8 + row_lane;
-      const bool live = row < cu.k.rows && cu.r.end != 0;
-      const int tok = (cu.k.row0 + row) / P.group, g = (cu.k.row0 + row) - tok * P.group;
-      const uint16_t* src = P.q + (cu.q_off + tok) * P.q_ts +
-                            static_cast<int64_t>(cu.head * P.group + g) * P.q_hs;
-      const bool there = live && cu.q_off + tok < P.n_tokens;
-      float amax = 0.0f;
-      uint32_t raw[DP / 8];
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        const int d = col_lane * (DP / 4) + i * 8;
-        if (there && d < P.c.head_dim) x = *reinterpret_cast<const uint4*>(src + d);
-        raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
-      }
-      float unit = 1.0f;
-      if (P.bf16) {
-        // To fp16 by way of a power of two that puts the row's largest in [1, 2).
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          const float2 x = Pair<T>::unpack(raw[i]);
-          amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-        const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-        if (e > 0 && e < 254) unit = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          const float2 x = Pair<T>::unpack(raw[i]);
-          raw[i] = Pair<__half>::pack(x.x * unit, x.y * unit);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i) qf[nt][i] = raw[i];
-      // The products' columns of this thread: rows 2 col_lane and the next.
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * col_lane + c;
-        cf[nt][c] = P.scale_log2 / __shfl_sync(kFull, unit, (2 * col_lane + c) * 4);
-        const int p = cu.r.cached + (cu.k.row0 + r) / P.group;
-        // (A row that is not there sees everything: it must not keep m waiting.)
-        hi[nt][c] = r < cu.k.rows ? min(p, cu.k.end - 1) : INT32_MAX;
-        lo[nt][c] = r < cu.k.rows ? cu.r.begin : 0;
-        if (P.window > 0 && r < cu.k.rows) lo[nt][c] = max(lo[nt][c], p - P.window + 1);
-        if (r < cu.k.rows) {
-          all_hi = min(all_hi, hi[nt][c]);
-          all_lo = max(all_lo, lo[nt][c]);
-        }
-        m[nt][c] = -INFINITY;
-        l[nt][c] = 0.0f;
-      }
-#pragma unroll
-      for (int d = 0; d < DP / 16; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[d][nt][i] = 0.0f;
+    for (int i = 0; i < DP / 32; ++i) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      const int d = col_lane * (DP / 4) + i * 8;
+      if (there && d < P.c.head_dim) x = *reinterpret_cast<const uint4*>(src + d);
+      raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
     }
+    float unit = 1.0f;
+    if (P.bf16) {
+      // To fp16 by way of a power of two that puts the row's largest in [1, 2).
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        const float2 x = Pair<T>::unpack(raw[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+      const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+      if (e > 0 && e < 254) unit = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        const float2 x = Pair<T>::unpack(raw[i]);
+        raw[i] = Pair<__half>::pack(x.x * unit, x.y * unit);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i) qf[i] = raw[i];
+    // The products' columns of this thread: rows 2 col_lane and the next.
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 2 * col_lane + c;
+      cf[c] = P.scale_log2 / __shfl_sync(kFull, unit, (2 * col_lane + c) * 4);
+      const int p = cu.r.cached + (cu.k.row0 + r) / P.group;
+      // (A row that is not there sees everything: it must not keep m waiting.)
+      hi[c] = r < cu.k.rows ? min(p, cu.k.end - 1) : INT32_MAX;
+      lo[c] = r < cu.k.rows ? cu.r.begin : 0;
+      if (P.window > 0 && r < cu.k.rows) lo[c] = max(lo[c], p - P.window + 1);
+      if (r < cu.k.rows) {
+        all_hi = min(all_hi, hi[c]);
+        all_lo = max(all_lo, lo[c]);
+      }
+      m[c] = -INFINITY;
+      l[c] = 0.0f;
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] = 0.0f;
     all_hi = __reduce_min_sync(kFull, all_hi);
     all_lo = __reduce_max_sync(kFull, all_lo);
 
@@ -385,13 +394,11 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       ++used;
       // ---- S^T = K Q^T, two tiles of 16 positions
       constexpr int kM = kStep / 16;
-      float s[kM][NT][4];
+      float s[kM][4];
 #pragma unroll
       for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) s[mt][i] = 0.0f;
 #pragma unroll
       for (int w = 0; w < DP / 64; ++w) {
         const int ch = col_lane * (DP / 64) + w;
@@ -404,9 +411,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           for (int j = 0; j < 4; ++j) {
             const uint32_t a0 = e4m3x2_to_f16x2(aw[j]), a2 = e4m3x2_to_f16x2(aw[j] >> 16);
             const uint32_t a1 = e4m3x2_to_f16x2(bw[j]), a3 = e4m3x2_to_f16x2(bw[j] >> 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][8 * w + 2 * j], qf[nt][8 * w + 2 * j + 1]);
+            mma16816(s[mt], a0, a1, a2, a3, qf[8 * w + 2 * j], qf[8 * w + 2 * j + 1]);
           }
         }
       }
@@ -420,78 +425,66 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       }
       const bool partial = base < all_lo || base + kStep - 1 > all_hi;  // uniform
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int i = 0; i < 2 * kM; ++i) {
-            float& x = s[i >> 1][nt][2 * (i & 1) + c];
-            x *= ks[i] * cf[nt][c];
-            if (partial) {
-              const int p = base + 8 * i + row_lane;
-              if (p < lo[nt][c] || p > hi[nt][c]) x = -INFINITY;
-            }
+        for (int i = 0; i < 2 * kM; ++i) {
+          float& x = s[i >> 1][2 * (i & 1) + c];
+          x *= ks[i] * cf[c];
+          if (partial) {
+            const int p = base + 8 * i + row_lane;
+            if (p < lo[c] || p > hi[c]) x = -INFINITY;
           }
         }
       }
       // Weights under the references as they are; where their sum passes the
       // limit, or a row has no reference yet, m moves and they are done again.
-      float pw[kM][NT][4], part[NT][2];
+      float pw[kM][4], part[2];
       for (bool moved = false;; moved = true) {
         bool past = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int c = 0; c < 2; ++c) {
+          const float ref = m[c] == -INFINITY ? 0.0f : m[c];
+          float held = 0.0f;
+          part[c] = 0.0f;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float ref = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
-            float held = 0.0f;
-            part[nt][c] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2 * kM; ++i) {
-              const float w = ex2(s[i >> 1][nt][2 * (i & 1) + c] - ref);
-              part[nt][c] += w;
-              const float x = w * vs[i];
-              held += x;
-              pw[i >> 1][nt][2 * (i & 1) + c] = x;
-            }
-            past = past || !(held <= kLimit) || m[nt][c] == -INFINITY;
+          for (int i = 0; i < 2 * kM; ++i) {
+            const float w = ex2(s[i >> 1][2 * (i & 1) + c] - ref);
+            part[c] += w;
+            const float x = w * vs[i];
+            held += x;
+            pw[i >> 1][2 * (i & 1) + c] = x;
           }
+          past = past || !(held <= kLimit) || m[c] == -INFINITY;
         }
         if (moved || !__any_sync(kFull, past)) break;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int c = 0; c < 2; ++c) {
+          float t = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float t = -INFINITY;
+          for (int i = 0; i < 2 * kM; ++i)
+            t = fmaxf(t, s[i >> 1][2 * (i & 1) + c] + lg2(fmaxf(vs[i], 5.42101086e-20f)));
+          t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+          // (The same in all lanes that hold the row's columns.)
+          const float now = fmaxf(m[c], t);
+          const float f = now == -INFINITY ? 1.0f : ex2(m[c] - now);
+          m[c] = now;
+          l[c] *= f;
 #pragma unroll
-            for (int i = 0; i < 2 * kM; ++i)
-              t = fmaxf(t, s[i >> 1][nt][2 * (i & 1) + c] + lg2(fmaxf(vs[i], 5.42101086e-20f)));
-            t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
-            // (The same in all lanes that hold the row's columns.)
-            const float now = fmaxf(m[nt][c], t);
-            const float f = now == -INFINITY ? 1.0f : ex2(m[nt][c] - now);
-            m[nt][c] = now;
-            l[nt][c] *= f;
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-              o[d][nt][c] *= f;
-              o[d][nt][2 + c] *= f;
-            }
+          for (int d = 0; d < DP / 16; ++d) {
+            o[d][c] *= f;
+            o[d][2 + c] *= f;
           }
         }
       }
-      uint32_t pf[kM][NT][2];
+      uint32_t pf[kM][2];
+      l[0] += part[0];
+      l[1] += part[1];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] += part[nt][0];
-        l[nt][1] += part[nt][1];
-#pragma unroll
-        for (int i = 0; i < 2 * kM; ++i)
-          pf[i >> 1][nt][i & 1] = transpose8x8(Pair<__half>::pack(pw[i >> 1][nt][2 * (i & 1)],
-                                                                  pw[i >> 1][nt][2 * (i & 1) + 1]));
-      }
+      for (int i = 0; i < 2 * kM; ++i)
+        pf[i >> 1][i & 1] = transpose8x8(Pair<__half>::pack(pw[i >> 1][2 * (i & 1)],
+                                                                pw[i >> 1][2 * (i & 1) + 1]));
       // ---- O^T += V^T P^T.  A transposed 8x8 of byte pairs holds, for one
       // pair of channels, two positions; the two channels go to rows r and
       // r + 8 of the product.
@@ -527,23 +520,20 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
                   na[2 * j] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0020));
                   na[2 * j + 1] = e4m3x2_to_f16x2(__byte_perm(ones, 0u, 0x0031));
                 }
+                float seen[4];
+                const int p0 = base + 16 * mt + row_lane, p1 = p0 + 8;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float seen[4];
-                  const int p0 = base + 16 * mt + row_lane, p1 = p0 + 8;
-#pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    seen[c] = (p0 >= lo[nt][c] && p0 <= hi[nt][c]) ? 1.0f : 0.0f;
-                    seen[2 + c] = (p1 >= lo[nt][c] && p1 <= hi[nt][c]) ? 1.0f : 0.0f;
-                  }
-                  const uint32_t b0 = transpose8x8(Pair<__half>::pack(seen[0], seen[1]));
-                  const uint32_t b1 = transpose8x8(Pair<__half>::pack(seen[2], seen[3]));
-                  float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma16816(hit, na[0], na[1], na[2], na[3], b0, b1);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (hit[i] > 0.0f) o[2 * d2 + k][nt][i] = __uint_as_float(0x7fffffffu);
+                for (int c = 0; c < 2; ++c) {
+                  seen[c] = (p0 >= lo[c] && p0 <= hi[c]) ? 1.0f : 0.0f;
+                  seen[2 + c] = (p1 >= lo[c] && p1 <= hi[c]) ? 1.0f : 0.0f;
                 }
+                const uint32_t b0 = transpose8x8(Pair<__half>::pack(seen[0], seen[1]));
+                const uint32_t b1 = transpose8x8(Pair<__half>::pack(seen[2], seen[3]));
+                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma16816(hit, na[0], na[1], na[2], na[3], b0, b1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (hit[i] > 0.0f) o[2 * d2 + k][i] = __uint_as_float(0x7fffffffu);
               }
             }
           }
@@ -553,9 +543,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
             const uint32_t y = __byte_perm(vw[2 * k + 1], 0u, 0x3120);
             const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_to_f16x2(x >> 16);
             const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(o[2 * d2 + k][nt], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
+            mma16816(o[2 * d2 + k], a0, a1, a2, a3, pf[mt][0], pf[mt][1]);
           }
         }
       }
@@ -565,15 +553,12 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
 
     // ---- the block's end, or the range's
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float t = l[nt][c];
-        t += __shfl_xor_sync(kFull, t, 4);
-        t += __shfl_xor_sync(kFull, t, 8);
-        t += __shfl_xor_sync(kFull, t, 16);
-        l[nt][c] = t;
-      }
+    for (int c = 0; c < 2; ++c) {
+      float t = l[c];
+      t += __shfl_xor_sync(kFull, t, 4);
+      t += __shfl_xor_sync(kFull, t, 8);
+      t += __shfl_xor_sync(kFull, t, 16);
+      l[c] = t;
     }
     auto lse_of = [](float mm, float ll) {
       return ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
@@ -587,22 +572,19 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     };
     if (whole) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int c = 0; c < 2; ++c) {
+        int64_t j;
+        int h;
+        if (!place(2 * col_lane + c, &j, &h)) continue;
+        const float inv = l[c] != 0.0f ? (1.0f / kUnit) / l[c] : 0.0f;  // NaN stays NaN
+        uint16_t* dst = P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + 2 * row_lane;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          int64_t j;
-          int h;
-          if (!place(nt * 8 + 2 * col_lane + c, &j, &h)) continue;
-          const float inv = l[nt][c] != 0.0f ? (1.0f / kUnit) / l[nt][c] : 0.0f;  // NaN stays NaN
-          uint16_t* dst = P.out + j * P.o_ts + static_cast<int64_t>(h) * P.o_hs + 2 * row_lane;
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d)
-            if (d * 16 < P.c.head_dim)
-              *reinterpret_cast<uint32_t*>(dst + d * 16) =
-                  Pair<T>::pack(o[d][nt][c] * inv, o[d][nt][2 + c] * inv);
-          if (row_lane == 0 && P.lse != nullptr)
-            P.lse[j * P.q_heads + h] = lse_of(m[nt][c], l[nt][c]);
-        }
+        for (int d = 0; d < DP / 16; ++d)
+          if (d * 16 < P.c.head_dim)
+            *reinterpret_cast<uint32_t*>(dst + d * 16) =
+                Pair<T>::pack(o[d][c] * inv, o[d][2 + c] * inv);
+        if (row_lane == 0 && P.lse != nullptr)
+          P.lse[j * P.q_heads + h] = lse_of(m[c], l[c]);
       }
     } else {
       // Partial slots: 0 for a block that began in an earlier warp, 1 for one
@@ -610,18 +592,15 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       constexpr int kFloats = partial_floats(kRows, DP);
       float* mine = P.partials + (2 * worker + (t_begin == 0 ? 1 : 0)) * kFloats;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int c = 0; c < 2; ++c) {
+        const int r = 2 * col_lane + c;
+        if (r >= cu.k.rows) continue;
+        float* dst = mine + r * DP + 2 * row_lane;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = nt * 8 + 2 * col_lane + c;
-          if (r >= cu.k.rows) continue;
-          float* dst = mine + r * DP + 2 * row_lane;
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d)
-            __stcg(reinterpret_cast<float2*>(dst + d * 16), make_float2(o[d][nt][c], o[d][nt][2 + c]));
-          if (row_lane == 0)
-            __stcg(reinterpret_cast<float2*>(mine + kRows * DP) + r, make_float2(m[nt][c], l[nt][c]));
-        }
+        for (int d = 0; d < DP / 16; ++d)
+          __stcg(reinterpret_cast<float2*>(dst + d * 16), make_float2(o[d][c], o[d][2 + c]));
+        if (row_lane == 0)
+          __stcg(reinterpret_cast<float2*>(mine + kRows * DP) + r, make_float2(m[c], l[c]));
       }
       int64_t c0, c1;
       block_workers(range, cu, &c0, &c1);
@@ -683,10 +662,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
   grid_dependency_wait();  // this grid ends no sooner than the tile kernel's
 }
 
-template <typename T, int DP, int NT>
+template <typename T, int DP>
 cudaError_t launch(const AttendParams& P, int ctas, bool beside, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0ull};
-  const auto kernel = attend_rows_kernel<T, DP, NT>;
+  const auto kernel = attend_rows_kernel<T, DP>;
   constexpr int bytes = Layout<DP>::kBytes;
   const cudaError_t e = set_smem_limit_once(done, kernel, bytes);
   if (e != cudaSuccess) return e;
@@ -706,30 +685,20 @@ cudaError_t launch(const AttendParams& P, int ctas, bool beside, cudaStream_t st
 }
 
 template <typename T>
-cudaError_t launch_type(const AttendParams& P, int rows, int ctas, bool beside,
-                        cudaStream_t stream) {
-  const bool wide = P.c.head_dim > 64;
-  if (rows == 8)
-    return wide ? launch<T, 128, 1>(P, ctas, beside, stream)
-                : launch<T, 64, 1>(P, ctas, beside, stream);
-  return wide ? launch<T, 128, 2>(P, ctas, beside, stream)
-              : launch<T, 64, 2>(P, ctas, beside, stream);
+cudaError_t launch_type(const AttendParams& P, int ctas, bool beside, cudaStream_t stream) {
+  return P.c.head_dim > 64 ? launch<T, 128>(P, ctas, beside, stream)
+                           : launch<T, 64>(P, ctas, beside, stream);
 }
 
 }  // namespace
 
-int row_block(int max_q_len, int group) {
-  return static_cast<int64_t>(max_q_len) * group <= 8 ? 8 : 16;
+size_t row_partial_bytes(int ctas, int head_dim) {
+  return static_cast<size_t>(ctas) * kWarps * 2 * partial_floats(kRows, head_dim > 64 ? 128 : 64) * 4;
 }
 
-size_t row_partial_bytes(int rows, int ctas, int head_dim) {
-  return static_cast<size_t>(ctas) * kWarps * 2 * partial_floats(rows, head_dim > 64 ? 128 : 64) * 4;
-}
-
-cudaError_t launch_attend_rows(const AttendParams& P, int rows, int ctas, bool beside,
-                               cudaStream_t stream) {
-  return P.bf16 ? launch_type<__nv_bfloat16>(P, rows, ctas, beside, stream)
-                : launch_type<__half>(P, rows, ctas, beside, stream);
+cudaError_t launch_attend_rows(const AttendParams& P, int ctas, bool beside, cudaStream_t stream) {
+  return P.bf16 ? launch_type<__nv_bfloat16>(P, ctas, beside, stream)
+                : launch_type<__half>(P, ctas, beside, stream);
 }
 
 }  // namespace pkv
