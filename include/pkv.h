@@ -556,7 +556,8 @@ size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_le
  *   x = x - frequency[b] * c - (c > 0 ? presence[b] : 0)
  *   x = x + the biases of v, one after another in list order
  *   x = -inf                                   if v's bit in the mask is 0
- * in fp32, rounded once to the logits' type.  Row b's biases are the pairs
+ * in fp32 (the quotient as a product with 1 / repetition), rounded once to the
+ * logits' type.  Row b's biases are the pairs
  * (bias_ids[e], bias_values[e]), bias_ptr[b] <= e < bias_ptr[b + 1].  Bit
  * v % 32 of mask[b * mask_stride + v / 32] is v's.  A masked place is -inf
  * whatever was there, NaN included.  An element that no rule touches keeps

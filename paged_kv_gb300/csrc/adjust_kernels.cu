@@ -117,7 +117,8 @@ struct Row {
 template <int BITS>
 __device__ __forceinline__ float penalise(const Row& r, float x, uint32_t cell) {
   // A product with the reciprocal: both are rounded to 32 bits, so it is within
-  // 1.5 units in the last place of the quotient (a division for each element of
+  // 1.5 units in the last place of the quotient for repetitions of 2^-126 to
+  // 2^126 (a division for each element of
   // the stream costs 20 times the instructions).  Without branches: the choice
   // at the end leaves an unnamed token as it is, whatever the penalties hold.
   const float count = static_cast<float>(cell & CellOf<BITS>::kCount);
@@ -347,8 +348,11 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
             if ((lo | hi) == 0u) continue;
             const float x = penalise<BITS>(r, __uint_as_float(w[k] << 16), lo);
             const float y = penalise<BITS>(r, __uint_as_float(w[k] & 0xffff0000u), hi);
-            w[k] = __bfloat16_as_ushort(__float2bfloat16_rn(x)) |
-                   static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(y))) << 16;
+            const uint32_t z = __bfloat16_as_ushort(__float2bfloat16_rn(x)) |
+                               static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(y))) << 16;
+            // (Rounding would change a NaN's bits, and the other one may be no one's.)
+            const uint32_t keep = (lo != 0u ? 0u : 0xffffu) | (hi != 0u ? 0u : 0xffff0000u);
+            w[k] = (z & ~keep) | (w[k] & keep);
           }
         }
       }

@@ -148,6 +148,31 @@ def test_values_that_are_not_finite(inplace):
     assert torch.equal(got == math.inf, want == math.inf)
 
 
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_what_no_rule_names_keeps_its_bits(dt, inplace):
+    # NaNs of every payload and sign beside named tokens, in every place of a vector.
+    v = 4096
+    bits = torch.arange(v, dtype=torch.int32)
+    if dt == torch.bfloat16:
+        raw = (0x7F81 + bits % 126 + (bits % 2) * 0x8000).to(torch.int32).to(torch.int16)
+    else:
+        raw = (0x7F800001 + bits * 1021) | torch.where(bits % 2 == 1, -2 ** 31, 0).to(torch.int32)
+    named = torch.arange(0, v, 3, dtype=torch.int32)
+    logits = raw.view(dt)[None].clone()
+    p = dict(token_pool=named[None].contiguous(), table_idx=torch.zeros(1, dtype=torch.int32),
+             prompt_len=torch.tensor([700], dtype=torch.int32),
+             device_len=torch.tensor([named.numel()], dtype=torch.int32),
+             repetition=torch.tensor([1.5]), frequency=torch.tensor([0.5]),
+             presence=torch.tensor([0.25]))
+    x = logits.to(DEV)
+    got = pkv.adjust_logits(x, out=None if inplace else torch.empty_like(x), **dev(p)).cpu()
+    other = torch.ones(v, dtype=torch.bool)
+    other[named.long()] = False
+    assert torch.equal(got.view(raw.dtype)[0, other], raw[other])
+    assert bool(torch.isnan(got).all())
+
+
 def test_bad_rows_are_reported_and_skipped():
     logits, p = problem(4, 500, 40, 6, 45, torch.float32, "rpfb")
     good = dict(p)
