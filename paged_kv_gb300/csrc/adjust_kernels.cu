@@ -22,7 +22,7 @@
 // Bound: bytes (out of place: one read and one write of the logits).  For 256 x
 // 151936 bf16 (histories to 2512 tokens, 64 biases a row, a third of the rows
 // masked) 44 us, 3.7 TB/s; for 1024 x 256000 bf16 (histories to 36863 tokens,
-// 300 biases a row) 415 us, 2.8 TB/s, of which the histories take half: every
+// 300 biases a row) 428 us, 2.7 TB/s, of which the histories take half: every
 // slice of a row reads them all (150 us, the latency of those reads more than
 // their count), atomics on the frequent tokens 40, penalties in the stream 60.
 // Measured against this for the second size: two CTAs an SM with 96 KB of cells
@@ -51,6 +51,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kUnroll = 4;
 constexpr int kCellBytes = 64 * 1024;  // shared memory of the cells: three CTAs an SM
+constexpr int kPadBytes = 32;          // and what aligns them
 constexpr int kMaxCount16 = 16383;
 constexpr int kBiasCap = kThreads;     // gathered biases of a slice
 
@@ -72,7 +73,6 @@ struct AdjustParams {
   int32_t* status;
   int64_t pool_rows, pool_cols, n_bias, mask_stride;
   int B, V, slice, slices;
-  bool vec;       // 16-byte accesses are aligned on both sides
 };
 
 template <int BITS> struct CellOf;
@@ -141,13 +141,35 @@ template <typename T> __device__ __forceinline__ uint32_t minus_inf_word();
 template <> __device__ __forceinline__ uint32_t minus_inf_word<float>() { return 0xff800000u; }
 template <> __device__ __forceinline__ uint32_t minus_inf_word<__nv_bfloat16>() { return 0xff80ff80u; }
 
+// How the logits are gone over: in place; out of place with every row on a
+// 16-byte boundary; or anywhere.  (With rows anywhere the second's code would do,
+// but 256 x 151936 take 44 us with it instead of 42, 1024 x 256000 446 instead of
+// 420; 404 x 115753 fp32 take 71 us, and 146 element by element.)
+enum class Way { kInPlace, kAligned, kAnywhere };
+
 // The tokens [v0, v1) of one row.
-template <typename T, int BITS, bool INPLACE>
+template <typename T, int BITS, Way WAY>
 __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T* out, int v0,
                              int v1, uint32_t* cells, int* s_id, float* s_val, int* s_count, int bad) {
   using C = CellOf<BITS>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int nv = v1 - v0;
+  // Vectors begin `head` tokens in, where the row reaches a 16-byte boundary (on
+  // both sides, or there are none).  Cells lie `pad` further on, so
+  // that a vector's cells are aligned too.
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr bool INPLACE = WAY == Way::kInPlace;
+  int head = 0, pad = 0, vecs = nv / kVec;
+  if (WAY == Way::kAnywhere) {
+    vecs = 0;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in + v0);
+    if (((a ^ reinterpret_cast<uintptr_t>(out + v0)) & 15) == 0) {
+      head = static_cast<int>((16 - (a & 15)) & 15) / static_cast<int>(sizeof(T));
+      pad = head == 0 ? 0 : kVec - head;
+      head = min(head, nv);
+      vecs = (nv - head) / kVec;
+    }
+  }
   const bool counted = r.len > 0;
   const bool biased = r.bias_end > r.bias_begin;
   int listed = 0;  // biases of the slice
@@ -159,15 +181,15 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
   if (r.bias_begin + tid < r.bias_end)
     id = P.bias_ids[r.bias_begin + tid], val = P.bias_values[r.bias_begin + tid];
   if (counted) {
-    const int words = (nv * (BITS / 8) + 15) / 16;
+    const int words = ((nv + pad) * (BITS / 8) + 15) / 16;
     for (int i = tid; i < words; i += kThreads)
       reinterpret_cast<uint4*>(cells)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     auto one = [&](int tok, bool made) {
       const uint32_t i = static_cast<uint32_t>(tok - v0);
       if (i >= static_cast<uint32_t>(nv)) return;
-      if (made) cell_add<BITS>(cells, i, 1u);
-      else cell_or<BITS>(cells, i, C::kSeen);
+      if (made) cell_add<BITS>(cells, i + pad, 1u);
+      else cell_or<BITS>(cells, i + pad, C::kSeen);
     };
     auto note = [&](int tok, int at) { one(tok, at >= r.prompt); };
     // 16-byte loads from the first aligned entry on; nearly every four lie on
@@ -229,7 +251,7 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
   auto penalty = [&](int v, float x) {
     if (!counted) return x;
     return penalise<BITS>(
-        r, x, INPLACE ? cell_take<BITS>(cells, v - v0) : cell_get<BITS>(cells, v - v0));
+        r, x, INPLACE ? cell_take<BITS>(cells, v - v0) : cell_get<BITS>(cells, v - v0 + pad));
   };
   const T* src = INPLACE ? out : in;
   int mine = -1;
@@ -297,23 +319,36 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
   }
 
   // ---- out of place: the slice once through
-  constexpr int kVec = 16 / sizeof(T);
   constexpr uint32_t kAll = (1u << kVec) - 1u;
-  const int vecs = P.vec ? nv / kVec : 0;
+  const int first = v0 + head;
+  const bool split = WAY == Way::kAnywhere && r.mask != nullptr;  // vectors may span two mask words
+  const uint32_t* own = cells + (head + pad) * BITS / 32;  // the first vector's cells
   for (int i0 = tid; i0 < vecs; i0 += kThreads * kUnroll) {
     uint4 raw[kUnroll];
     uint32_t bits[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads, v = v0 + i * kVec;
+      const int i = i0 + u * kThreads, v = first + i * kVec;
       bits[u] = kAll;
-      if (i < vecs && r.mask != nullptr) bits[u] = (r.mask[v >> 5] >> (v & 31)) & kAll;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < vecs && bits[u] != 0u) raw[u] = ld_stream_v4(in + v);
+      if (i < vecs && r.mask != nullptr) bits[u] = r.mask[v >> 5] >> (v & 31);
+    }
+    if (split) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kThreads, v = first + i * kVec;
+        if (i < vecs && (v & 31) > 32 - kVec) bits[u] |= r.mask[(v >> 5) + 1] << (32 - (v & 31));
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads, at = i * kVec;
+      const int i = i0 + u * kThreads;
+      bits[u] &= kAll;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < vecs && bits[u] != 0u) raw[u] = ld_stream_v4(in + first + i * kVec);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads;
       if (i >= vecs) break;
       constexpr int kWords = kVec * BITS / 32;  // of cells
       uint32_t cw[kWords];
@@ -322,11 +357,11 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
       for (int k = 0; k < kWords; k += kWords < 4 ? 2 : 4) {
         if (kWords < 4) {
           uint2 c = make_uint2(0u, 0u);
-          if (counted) c = *reinterpret_cast<const uint2*>(cells + at * BITS / 32);
+          if (counted) c = *reinterpret_cast<const uint2*>(own + i * kWords);
           cw[k] = c.x, cw[k + 1] = c.y;
         } else {
           uint4 c = make_uint4(0u, 0u, 0u, 0u);
-          if (counted) c = *reinterpret_cast<const uint4*>(cells + at * BITS / 32 + k);
+          if (counted) c = *reinterpret_cast<const uint4*>(own + i * kWords + k);
           cw[k] = c.x, cw[k + 1] = c.y, cw[k + 2] = c.z, cw[k + 3] = c.w;
         }
       }
@@ -370,13 +405,13 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
           w[k] = (w[k] & ~hide) | (inf & hide);
         }
       }
-      *reinterpret_cast<uint4*>(out + v0 + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(out + first + i * kVec) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  for (int i = vecs * kVec + tid; i < nv; i += kThreads) {
-    const int v = v0 + i;
+  for (int e = tid; e < nv - vecs * kVec; e += kThreads) {
+    const int i = e < head ? e : e + vecs * kVec, v = v0 + i;
     T x = in[v];
-    const uint32_t c = counted ? cell_get<BITS>(cells, i) : 0u;
+    const uint32_t c = counted ? cell_get<BITS>(cells, i + pad) : 0u;
     if (!allowed(r, v)) store_one(&x, -INFINITY);
     else if (c != 0u) store_one(&x, penalise<BITS>(r, load_one(&x), c));
     out[v] = x;
@@ -387,7 +422,7 @@ __device__ void adjust_range(const AdjustParams& P, const Row& r, const T* in, T
   }
 }
 
-template <typename T, bool INPLACE>
+template <typename T, Way WAY>
 __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(const AdjustParams P) {
   extern __shared__ __align__(16) uint32_t cells[];
   __shared__ __align__(16) int s_id[kBiasCap];
@@ -427,29 +462,33 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(const AdjustParams 
     else r.bias_begin = e0, r.bias_end = e1;
   }
   if (r.len - r.prompt <= kMaxCount16) {
-    adjust_range<T, 16, INPLACE>(P, r, in, out, v0, v1, cells, s_id, s_val, s_count, bad);
+    adjust_range<T, 16, WAY>(P, r, in, out, v0, v1, cells, s_id, s_val, s_count, bad);
   } else {
     const int mid = min(v1, v0 + P.slice / 2);
-    adjust_range<T, 32, INPLACE>(P, r, in, out, v0, mid, cells, s_id, s_val, s_count, bad);
+    adjust_range<T, 32, WAY>(P, r, in, out, v0, mid, cells, s_id, s_val, s_count, bad);
     __syncthreads();
     if (mid < v1)
-      adjust_range<T, 32, INPLACE>(P, r, in, out, mid, v1, cells, s_id, s_val, s_count, bad);
+      adjust_range<T, 32, WAY>(P, r, in, out, mid, v1, cells, s_id, s_val, s_count, bad);
   }
 }
 
-template <typename T, bool INPLACE>
+template <typename T, Way WAY>
 cudaError_t launch(const AdjustParams& P, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0ull};
-  const auto kernel = adjust_kernel<T, INPLACE>;
-  const cudaError_t e = set_smem_limit_once(done, kernel, kCellBytes);
+  const auto kernel = adjust_kernel<T, WAY>;
+  const cudaError_t e = set_smem_limit_once(done, kernel, kCellBytes + kPadBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(P.B) * P.slices, kThreads, P.slice * 2, s>>>(P);
+  kernel<<<static_cast<unsigned>(P.B) * P.slices, kThreads, P.slice * 2 + kPadBytes, s>>>(P);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_type(const AdjustParams& P, cudaStream_t s) {
-  return P.logits == P.out ? launch<T, true>(P, s) : launch<T, false>(P, s);
+  if (P.logits == P.out) return launch<T, Way::kInPlace>(P, s);
+  constexpr int kVec = 16 / sizeof(T);
+  const bool aligned = aligned16(P.logits) && aligned16(P.out) && P.in_stride % kVec == 0 &&
+                       P.out_stride % kVec == 0;
+  return aligned ? launch<T, Way::kAligned>(P, s) : launch<T, Way::kAnywhere>(P, s);
 }
 
 }  // namespace
@@ -522,8 +561,6 @@ extern "C" int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dty
   P.n_bias = n_bias;
   P.mask_stride = mask_stride;
   P.B = B, P.V = V;
-  P.vec = aligned16(logits) && aligned16(out) && (row_stride * elt) % 16 == 0 &&
-          (out_stride * elt) % 16 == 0;
   // Slices: as few as the cells allow, but enough for two CTAs an SM (otherwise
   // 4 x 32000 fp32 takes 7.9 us instead of 4.6, 16 x 151936 bf16 8.7 of 6.9); a
   // multiple of 2048 tokens, so that no mask word or vector straddles two

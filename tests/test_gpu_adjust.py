@@ -134,6 +134,28 @@ def test_strides_that_are_not_aligned(dt):
     assert bool((wide[:, :3] == 9.0).all()) and bool((wide[:, 2053:] == 9.0).all())
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("at", range(8))
+@pytest.mark.parametrize("v", [1, 6, 37, 2049, 40003])
+def test_rows_that_begin_anywhere(v, at, dt):
+    """In and out at the same distance from a 16-byte boundary, and at another."""
+    logits, p = problem(3, v, 60, 5, 47, dt)
+    stride = v + 9
+    src = torch.full((4 * stride,), 9.0, dtype=dt, device=DEV)
+    x = src.as_strided((3, v), (stride, 1), at)
+    x.copy_(logits)
+    first = None
+    for o in (at, at + 1):
+        dst = torch.full((4 * stride,), 8.0, dtype=dt, device=DEV)
+        out = pkv.adjust_logits(x, out=dst.as_strided((3, v), (stride, 1), o), **dev(p))
+        check(out, logits, p)
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+        touched = torch.zeros(4 * stride, dtype=torch.bool, device=DEV)
+        touched.as_strided((3, v), (stride, 1), o).fill_(True)
+        assert bool((dst[~touched] == 8.0).all())
+
+
 @pytest.mark.parametrize("inplace", [True, False])
 def test_values_that_are_not_finite(inplace):
     logits, p = problem(2, 300, 20, 4, 44, torch.float32)
