@@ -339,6 +339,25 @@ def test_calls_of_different_shapes_share_a_workspace():
             assert torch.equal(call(p, c, q, workspace=shared)[0], want)
 
 
+@pytest.mark.parametrize("new,long", [(40, 700), (1, 60), ((1, 40), 150)], ids=str)
+def test_short_blocks_beside_a_long_one(new, long):
+    # The ranges of equal cost end within and at blocks' starts; both kernels in one call.
+    b = 36
+    new = [new] * b if isinstance(new, int) else [new[i % 2] for i in range(b)]
+    cached = [(7 * i) % 5 for i in range(b)]
+    new[b // 2] = long
+    cached[b - 1] = 3000
+    p = ref.page_problem(cached, new, 16, 2, 64, 71)
+    q = queries(sum(new), 2, 64, torch.bfloat16, 72)
+    cache = make_cache(p)
+    got, lse, status = call(p, cache, q)
+    assert status == 0
+    check(p, q, got, lse)
+    for _ in range(3):
+        again, lse2, _ = call(p, cache, q)
+        assert torch.equal(again, got) and torch.equal(lse2, lse)
+
+
 @pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
 @pytest.mark.parametrize("new", [1, 3, 130])
 @pytest.mark.parametrize("rising", [True, False])
