@@ -37,7 +37,7 @@
 // unit takes 3800 to 4200 clocks with both tiles in turn, and a block's change
 // about 20000.  2 x 4096 tokens over 4096 cached, 16 query and 8 cache heads of
 // 128, bf16: 430 us, 960 TFLOP/s, half of what a library product of that size
-// reaches; 48 chunks of 1 to 512 tokens over up to 2000: 254 us, 401 TFLOP/s.
+// reaches; 48 chunks of 1 to 512 tokens over up to 2000: 246 us, 414 TFLOP/s.
 //
 // Every wait ends: after kWaitTries a thread sets `dead`, with which all waits
 // return at once, the loops (whose lengths do not depend on data) run out,
