@@ -271,8 +271,9 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
     return p;
   };
   float ks[kPer], vs[kPer];
+  bool mixed = false;  // a group of this warp's positions spans pages
   auto resolve = [&](const Places& p, int slot) {  // byte offsets, and the scales' loads
-    bool mixed = false;
+    mixed = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       int64_t off = -1;
@@ -298,7 +299,6 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
       }
     }
     mixed = __any_sync(kFull, mixed);
-    if ((tid & 31) == 0) B->mixed[slot][tid >> 5] = mixed ? 1 : 0;
     if (tid == 0) B->partial[slot] = p.partial ? 1 : 0;
   };
   Ring kr, er;                 // K slots; the place slots being reused
@@ -311,14 +311,18 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
     float k0[kPer], v0[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) k0[i] = ks[i], v0[i] = vs[i];
+    const bool m0 = mixed;
     if (u + 1 < units) {
-      wait(B, &B->sc_empty[er.slot], er.phase ^ 1u);  // the values' warps are done with it
+      // The values' warps are done with it.  They alone: the softmax may still be
+      // units behind, so what it reads (scales, mixed) is written further below.
+      wait(B, &B->sc_empty[er.slot], er.phase ^ 1u);
       er.next(L::kSc);
       resolve(ahead, next);
       ahead = read_places();
     }
     // A unit kSc earlier is through its softmax once K's slot is free again.
     wait(B, &B->k_empty[kr.slot], kr.phase ^ 1u);
+    if ((tid & 31) == 0) B->mixed[slot][tid >> 5] = m0 ? 1 : 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (i == 0 || second) {

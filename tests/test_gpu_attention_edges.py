@@ -1,0 +1,110 @@
+"""pkv_paged_attention on the GPU at its edges: tables whose locations are no runs of a
+page, references that move several times a unit, requests past their bound, queries
+and scales at the ends of their ranges."""
+
+import math
+
+import pytest
+import torch
+
+import serving_reference as ref
+from paged_kv_gb300 import pkv
+from test_gpu_append import make_cache
+from test_gpu_attention import DEV, call, queries
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(p, q, sm_scale):
+    """ref.attend's values for causal calls, a (request, head) at a time."""
+    ps, hkv = p["k"].shape[1], p["k"].shape[2]
+    n, hq, d = q.shape
+    group = hq // hkv
+    out = {x: torch.zeros(n, hq, d, dtype=torch.float64) for x in ("out", "mass", "tail")}
+    out.update({x: torch.zeros(n, hq, dtype=torch.float64) for x in ("lse", "prod")})
+    at = 0
+    for i in range(len(p["cached_len"])):
+        c, e = int(p["cached_len"][i]), int(p["device_len"][i])
+        loc = p["page_table"][int(p["table_idx"][i]), :e].long()
+        page, off = loc // ps, loc % ps
+        rows = slice(at, at + e - c)
+        at += e - c
+        hide = torch.arange(e) > torch.arange(c, e)[:, None]
+        for h in range(hkv):
+            k, v = (p[x].float()[page, off, h].double()
+                    * p[x + "_scale"][page, h].double()[:, None] for x in "kv")
+            for g in range(h * group, (h + 1) * group):
+                x = q[rows, g].double()
+                s = (x @ k.T * sm_scale).masked_fill(hide, -math.inf)
+                top = s.amax(1, keepdim=True)
+                w = torch.exp(s - top)
+                z = w.sum(1, keepdim=True)
+                out["out"][rows, g] = (w @ v) / z
+                out["lse"][rows, g] = (top + z.log())[:, 0]
+                out["mass"][rows, g] = (w @ v.abs()) / z
+                out["tail"][rows, g] = ((~hide).double() @ v.abs()) / z
+                # (A sum over seen keys' channels bounds their largest product.)
+                out["prod"][rows, g] = (x.abs() @ k.abs().T * abs(sm_scale)).masked_fill(
+                    hide, 0.0).amax(1)
+    return out
+
+
+def check(want, q, got, lse):
+    tol, lse_tol = ref.attend_tolerance(want, q.dtype, q.shape[2])
+    err = (got - want["out"]).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    err = (lse - want["lse"]).abs()
+    assert bool((err <= lse_tol).all()), float((err / lse_tol).max())
+
+
+def set_channel(p, name, positions, channel, value):
+    """Channel ``channel`` of the keys or values at the first request's positions."""
+    loc = p["page_table"][int(p["table_idx"][0]), positions].long()
+    ps = p[name].shape[1]
+    x = p[name].float().clone()
+    x[loc // ps, loc % ps, :, channel] = torch.as_tensor(value)[..., None]
+    p[name] = x.to(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("odd_units", [(0, 1, 2, 3), (0,), (1, 6, 11), (3, 4, 9, 15)], ids=str)
+@pytest.mark.parametrize("bad", [False, True])
+def test_tables_that_are_no_runs_in_some_units(dt, odd_units, bad):
+    """Units of 128 positions whose groups of 16 mix pages (or begin with a location outside
+    the cache) among units of whole pages: each unit takes its own way."""
+    requests, cached, new, ps, hkv, d = 12, 2000, 150, 16, 8, 64
+    p = ref.page_problem([cached], [new], ps, hkv, d, 81)
+    g = torch.Generator().manual_seed(82)
+    for name in "kv":  # neighbouring pages differ by much
+        p[name + "_scale"] = torch.exp2(torch.randint(-9, -2, p[name + "_scale"].shape,
+                                                      generator=g).float())
+    row = int(p["table_idx"][0])
+    used = set((p["page_table"][row] // ps).tolist())
+    spare = next(x for x in range(p["num_pages"]) if x not in used)
+    for name in "kv":
+        x = p[name].float().clone()
+        x[spare] = 0.0
+        p[name] = x.to(torch.float8_e4m3fn)
+    given = dict(p, page_table=p["page_table"].clone())
+    p["page_table"] = p["page_table"].clone()
+    for u in odd_units:
+        span = slice(128 * u, 128 * u + 128)
+        if bad:
+            at = torch.arange(128 * u, 128 * u + 128, 16)
+            given["page_table"][row, at] = 1 << 30
+            p["page_table"][row, at] = spare * ps  # a zero key and value
+        else:
+            order = torch.randperm(128, generator=g)
+            for t in (p, given):
+                t["page_table"][row, span] = t["page_table"][row, span][order]
+    q = queries(new, 2 * hkv, d, dt, 83)
+    want = attend(p, q, d ** -0.5)
+    many = dict(given)  # the same request again and again: every CTA has many units
+    for name in ("cached_len", "device_len", "table_idx"):
+        many[name] = given[name].repeat(requests)
+    cache = make_cache(p)
+    for _ in range(4):
+        out, lse, status = call(many, cache, q.repeat(requests, 1, 1))
+        assert status == (pkv.ST_ROW_OOB if bad else 0)
+        for i in range(requests):
+            check(want, q, out[i * new:(i + 1) * new], lse[i * new:(i + 1) * new])
