@@ -4,9 +4,12 @@
 // A unit (attend_units.cuh) is 128 positions for a block of up to 256 rows of
 // one (request, cache head), held as two tiles of 128 rows.  Per unit and tile
 //   S[128 x 128] = Q K^T   on kind::f8f6f4: K's codes go to the tensor core as
-//     they are; a query row, scaled by a power of two, is the sum of NS e4m3
-//     rows, exactly: 4 significant bits each, so 2 for bf16 and 3 for fp16
-//     (elements below 2^-9 of a row's largest keep an absolute 2^-17 of it);
+//     they are; a query row, scaled by a power of two, is the sum of NS rows of
+//     8-bit codes: e4m3 (4 significant bits, which leave a signed rest of 4 bits
+//     less), the last one e5m2, whose 3 bits hold what is left and reach down to
+//     2^-16.  So 2 rows for bf16 and 3 for fp16 are the query exactly, but for
+//     elements below 2^-13 (bf16) or 2^-10 (fp16) of a row's largest, which keep
+//     an absolute 2^-21 of it;
 //   S times the page's key scale and the row's factor, softmax in fp32;
 //   O[128 x D] += P V      on kind::f16: V's codes made 16 bits wide (exactly) on
 //     their way to shared memory, P = 2^(s - m) vs in tensor memory, in S's
@@ -388,10 +391,15 @@ __device__ __forceinline__ void widen(const uint4& c, uint4& lo, uint4& hi) {
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Two fp16 values as e4m3 codes, to nearest.
+// Two fp16 values as 8-bit codes, to nearest.
 __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
@@ -487,8 +495,10 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
   using L = Plan<NS>;
   const uint32_t tmem = __shfl_sync(kFull, B->tmem, 0);
   const int ksteps = (P.c.head_dim + 31) >> 5;
-  const uint32_t qk_instr = tc::instruction(0, kTile, false);
-  const uint32_t pv_instr = tc::instruction(Weight<T>::type, P.c.head_dim, true);
+  const uint32_t qk_instr = tc::instruction(0, 0, kTile, false);
+  const uint32_t qk_last = tc::instruction(1, 0, kTile, false);  // e5m2 codes
+  const uint32_t pv_instr =
+      tc::instruction(Weight<T>::type, Weight<T>::type, P.c.head_dim, true);
   constexpr uint32_t kHi = tc::operand_hi(1024);
   const uint32_t q0 = tc::operand_lo(smem_addr(smem + L::q), 16);
   const uint32_t k0 = tc::operand_lo(smem_addr(smem + L::k), 16);
@@ -502,8 +512,8 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k < ksteps)
-          tc::mma8_ss(tmem + t * kTile, qd + s * (kQBytes / 16) + 2 * k, kd + 2 * k, kHi, qk_instr,
-                      s + k > 0);
+          tc::mma8_ss(tmem + t * kTile, qd + s * (kQBytes / 16) + 2 * k, kd + 2 * k, kHi,
+                      s + 1 < NS ? qk_instr : qk_last, s + k > 0);
       }
     }
   };
@@ -765,7 +775,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
     const bool there = live && j_row < P.n_tokens;
     const uint32_t rows_there = __ballot_sync(kFull, there);
     uint8_t* q = smem + L::q + t * NS * kQBytes;
-    // ---- the warp's queries, each as NS e4m3 rows.  They come as they are to
+    // ---- the warp's queries, each as NS rows of codes.  They come as they are to
     // the place of their first two codes (32 rows of 128 bytes in each: a row's
     // first and second half) and are converted there.  A half warp has a row and
     // a lane 8 channels of it.  The loops are rolled: this code runs once a
@@ -806,11 +816,12 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
             e > 8 && e < 255 ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 1.0f;
         const float f = __shfl_sync(kFull, unit, (lane & 1) * 16);  // (and all have read)
         if ((lane >> 1) == i) factor = f;
-        // The codes have no infinity: a row that is not finite is NaNs.
+        // Not all codes have an infinity: a row that is not finite is NaNs (0x7f in
+        // e4m3 and in e5m2).
         const uint32_t nans = e == 255 ? 0x7f7f7f7fu : 0u;
         // In fp16, whose 11 bits hold an element of either type and what is
-        // left of it after each code exactly (down to 2^-24, and the codes end
-        // at 2^-9).
+        // left of it after each code exactly (down to 2^-24; e4m3 codes end at
+        // 2^-9, e5m2 codes at 2^-16).
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const float2 z = Pair<T>::unpack(x[n]);
@@ -821,7 +832,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
           uint32_t o[4];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            o[n] = e4m3x2_of_f16x2(x[n]);
+            o[n] = s + 1 < NS ? e4m3x2_of_f16x2(x[n]) : e5m2x2_of_f16x2(x[n]);
             if (s + 1 < NS) x[n] = sub_f16x2(x[n], e4m3x2_to_f16x2(o[n]));
           }
           if (store)

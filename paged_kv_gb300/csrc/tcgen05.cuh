@@ -61,10 +61,11 @@ __host__ __device__ constexpr uint32_t operand_hi(uint32_t group) {
   return ((group >> 4) & 0x3fffu) | (1u << 14) | (2u << 29);
 }
 
-// 128 x n product into fp32; types: 0 e4m3 (8 bits) or fp16, 1 bf16 (16 bits).
-// b_wide: B's contiguous dimension is n, not the summed one.
-__host__ __device__ constexpr uint32_t instruction(int type, int n, bool b_wide) {
-  return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
+// 128 x n product into fp32; types of A and B: 8 bits 0 e4m3, 1 e5m2 (they may
+// differ), 16 bits 0 fp16, 1 bf16 (they may not).  b_wide: B's contiguous
+// dimension is n, not the summed one.
+__host__ __device__ constexpr uint32_t instruction(int a, int b, int n, bool b_wide) {
+  return (1u << 4) | (static_cast<uint32_t>(a) << 7) | (static_cast<uint32_t>(b) << 10) |
          (b_wide ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 

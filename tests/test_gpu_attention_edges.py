@@ -108,3 +108,21 @@ def test_tables_that_are_no_runs_in_some_units(dt, odd_units, bad):
         assert status == (pkv.ST_ROW_OOB if bad else 0)
         for i in range(requests):
             check(want, q, out[i * new:(i + 1) * new], lse[i * new:(i + 1) * new])
+
+
+@pytest.mark.parametrize("dt,small", [(torch.bfloat16, 2.0 ** -11), (torch.float16, 2.0 ** -7)],
+                         ids=["bf16", "fp16"])
+def test_small_query_elements_beside_a_large_one_in_prompt_chunks(dt, small):
+    """The largest element of a query meets zeros; the scores are the small ones'."""
+    p = ref.page_problem([200], [140], 16, 2, 64, 86)
+    p["k_scale"][:] = 1.0
+    set_channel(p, "k", torch.arange(340), 0, torch.zeros(340))
+    g = torch.Generator().manual_seed(87)
+    q = small * (1 + torch.rand(140, 4, 64, generator=g))
+    q = (q * torch.where(torch.rand(q.shape, generator=g) < 0.5, -1.0, 1.0)).to(dt)
+    q[..., 0] = 1.0
+    sm_scale = 5 / (small * 384)
+    want = attend(p, q, sm_scale)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
+    assert status == 0
+    check(want, q, out, lse)
