@@ -578,6 +578,7 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
 // instruction caches.)
 template <typename W>
 __device__ __noinline__ void rescale(uint32_t o_tmem, int d, uint32_t p_tmem, int done, float f) {
+  tc::wait_st();  // an earlier quarter of the unit has stored P, and perhaps O
 #pragma unroll 1
   for (int k = 0; k < d; k += 32) {
     uint32_t o[32];

@@ -126,3 +126,22 @@ def test_small_query_elements_beside_a_large_one_in_prompt_chunks(dt, small):
     out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
     assert status == 0
     check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("new", [5, 130, 300])
+def test_references_that_move_in_every_quarter_of_a_unit(dt, new):
+    """Scores rise by 32 (46 powers of two) every 32 positions: what a unit has summed, and
+    the weights that it has stored, are scaled down several times before it ends."""
+    p = ref.page_problem([448], [new], 16, 1, 64, 84)
+    q = queries(new, 1, 64, dt, 85, gain=0.05)
+    q[..., 0] = 8.0
+    p["k_scale"][:] = 1.0
+    step = (torch.arange(448 + new) // 32).clamp_max(14) * 32.0
+    set_channel(p, "k", torch.arange(448 + new), 0, step)
+    want = attend(p, q, 0.125)
+    cache = make_cache(p)
+    for _ in range(4):
+        out, lse, status = call(p, cache, q, sm_scale=0.125)
+        assert status == 0
+        check(want, q, out, lse)
