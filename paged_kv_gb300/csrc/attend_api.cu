@@ -107,6 +107,9 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   float* partials =
       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(sms));
   const bool tiles = has_tiles(max_q_len, group);
+  // Alone, the row kernel takes the longer requests too: all of them are past
+  // max_q_len, and get zeros.
+  P.row_most = tiles ? kRowLimit : INT32_MAX;
   cudaError_t e = cudaSuccess;
   if (tiles) {
     P.counters = counters + row_counters(sms);

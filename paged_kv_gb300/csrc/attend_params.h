@@ -48,6 +48,7 @@ struct AttendParams {
   int64_t pt_rows, pt_cols;
   int B, max_q_len;
   int q_heads, group;          // group: query heads per cache head
+  int row_most;                // rows of a request that the row kernel still takes
   int window;                  // 0: none
   float scale_log2;            // sm_scale * log2(e)
   bool bf16;

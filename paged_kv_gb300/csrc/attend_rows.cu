@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     const __grid_constant__ AttendParams P) {
   using L = Layout<DP>;
   constexpr int kChunks = DP / 16;
-  constexpr UnitShape kShape{kRows, kStep, 1, kRowLimit, kLeast, kLead};
+  const UnitShape kShape{kRows, kStep, 1, P.row_most, kLeast, kLead};
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row_lane = lane >> 2, col_lane = lane & 3;

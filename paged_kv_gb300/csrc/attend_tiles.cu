@@ -81,7 +81,7 @@ constexpr int kPart = 32;                // columns a softmax thread has in regi
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kWaitTries = 1 << 20;
 __host__ __device__ constexpr UnitShape unit_shape() {
-  return UnitShape{kBlockRows, kTile, kRowLimit + 1, int64_t{1} << 40, 1, kLead};
+  return UnitShape{kBlockRows, kTile, kRowLimit + 1, INT32_MAX, 1, kLead};
 }
 
 // P and V are of the queries' type.  An entry of P is `unit` 2^(s - m) vs, and

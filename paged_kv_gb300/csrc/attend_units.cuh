@@ -32,7 +32,7 @@ __device__ __forceinline__ void grid_dependency_wait() {
 
 struct UnitShape {
   int rows, tile;
-  int64_t min_rows, max_rows;
+  int min_rows, max_rows;
   int least;  // cost of a worker's range, where there is so much
   int lead;
 };
@@ -91,15 +91,16 @@ __device__ __forceinline__ Block make_block(const AttendParams& P, const Request
 // Blocks of one (request, cache head) that this kernel takes.
 __device__ __forceinline__ int block_count(const AttendParams& P, const Request& r,
                                            const UnitShape& u) {
-  const int64_t n = static_cast<int64_t>(r.q_len) * P.group;
+  const int n = r.q_len * P.group;  // (the host bounds n_tokens * q_heads by 2^31)
   if (n < u.min_rows || n > u.max_rows) return 0;
-  return static_cast<int>((n + u.rows - 1) / u.rows);
+  return (n - 1) / u.rows + 1;
 }
 
 __device__ __forceinline__ int64_t request_cost(const AttendParams& P, const Request& r,
                                                  const UnitShape& u) {
   const int nb = block_count(P, r, u);
   int64_t cost = static_cast<int64_t>(nb) * u.lead;
+  if (r.bad != 0) return (cost + nb) * P.c.kv_heads;  // (one empty tile a block)
   for (int b = 0; b < nb; ++b) cost += make_block(P, r, b, u).tiles;
   return cost * P.c.kv_heads;
 }
@@ -216,6 +217,10 @@ __device__ Range find_range(const AttendParams& P, const UnitShape& u, void* scr
       ++c->req;
     }
     c->block = 0;
+    if (c->r.bad != 0) {
+      c->block = static_cast<int>(at / (1 + u.lead));
+      at -= static_cast<long long>(c->block) * (1 + u.lead);
+    }
     for (;;) {
       c->k = make_block(P, c->r, c->block, u);
       if (at < c->k.tiles + u.lead) break;

@@ -145,3 +145,25 @@ def test_references_that_move_in_every_quarter_of_a_unit(dt, new):
         out, lse, status = call(p, cache, q, sm_scale=0.125)
         assert status == 0
         check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("group,new,most", [(16, [1, 3, 1, 40], 1), (2, [2, 100, 1], 2),
+                                            (1, [33, 4, 4000], 4), (8, [2, 5], 4)], ids=str)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_requests_of_many_rows_past_the_bound_get_zeros(dt, group, new, most):
+    """However many rows they have, and whichever kernels the bound asks for."""
+    p = ref.page_problem([20 * i for i in range(len(new))], new, 16, 2, 64, 88)
+    q = queries(sum(new), 2 * group, 64, dt, 89)
+    cache = make_cache(p)
+    out = torch.full(q.shape, 5.0, dtype=dt, device=DEV)
+    got, lse, status = call(p, cache, q, max_q_len=most, out=out)
+    assert status == pkv.ST_TOKEN_CAP
+    want = attend(p, q, 64 ** -0.5)
+    at = 0
+    for n in new:
+        rows = slice(at, at + n)
+        at += n
+        if n > most:
+            assert not got[rows].any() and bool((lse[rows] == -math.inf).all())
+        else:
+            check({x: y[rows] for x, y in want.items()}, q[rows], got[rows], lse[rows])
