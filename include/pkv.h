@@ -442,6 +442,10 @@ typedef struct {
 
 #define PKV_MAX_HEAD_DIM 128
 
+/* Bytes at the start of pkv_paged_attention's workspace that have to be zero
+ * before its first use. */
+#define PKV_ATTENTION_ZERO_BYTES 65536
+
 /*
  * pkv_append_kv -- writes a step's keys and values into the cache at the
  * locations out_loc (pkv_prepare_step's), rotating q and k by position.
@@ -524,8 +528,9 @@ int pkv_append_kv(const pkv_kv_cache* cache, const void* k, int64_t k_token_stri
  *   NULL; cached_len, device_len, table_idx [B] int32; kv_begin [B] int32 or
  *   NULL; page_table [pt_rows, pt_cols] int32; status device int32 or NULL;
  *   workspace of pkv_paged_attention_workspace_bytes(...) bytes, 16-byte
- *   aligned, zeroed before its first use; every call leaves it ready for the
- *   next on the same stream, and no two calls that may overlap share one.
+ *   aligned, its first PKV_ATTENTION_ZERO_BYTES zeroed before its first use;
+ *   every call leaves it ready for the next on the same stream, and no two
+ *   calls that may overlap share one.
  * Errors: PKV_EINVAL (NULL pointer, bad cache, dtype, sizes, B outside
  * [0, PKV_MAX_FILL_BATCH], q_heads not a multiple of kv_heads, strides or
  * pointers that leave a row unaligned to 16 bytes, sm_scale not finite,

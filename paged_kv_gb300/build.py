@@ -126,8 +126,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     os.replace(tmp, LIB)
     tmp = BINDING + f".{os.getpid()}.tmp"
     _run(["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L" + torch_lib, "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib],
-         "the binding's link", verbose)
+          "-ltorch_cpu", "-ltorch_python", "-L" + libdir, "-lcudart", "-Wl,-rpath,$ORIGIN",
+          "-Wl,-rpath," + torch_lib, "-Wl,-rpath," + libdir], "the binding's link", verbose)
     os.replace(tmp, BINDING)
     return LIB
 

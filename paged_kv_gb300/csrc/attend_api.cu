@@ -19,7 +19,7 @@ size_t workspace_need(int max_q_len, int group, int head_dim) {
   size_t partials = pkv::row_partial_bytes(pkv::row_ctas(sms), head_dim);
   if (pkv::has_tiles(max_q_len, group))
     partials += pkv::tile_partial_bytes(pkv::tile_ctas(sms), head_dim);
-  return pkv::counter_bytes(sms) + partials;
+  return pkv::kCounterBytes + partials;
 }
 
 }  // namespace
@@ -104,8 +104,8 @@ int pkv_paged_attention(const pkv_kv_cache* cache, const void* q, int64_t q_toke
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int sms = num_sms();
   uint32_t* counters = static_cast<uint32_t*>(workspace);
-  float* partials =
-      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(sms));
+  if (!counters_fit(sms)) return fail(PKV_EUNSUPPORTED, "%d SMs", sms);
+  float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
   const bool tiles = has_tiles(max_q_len, group);
   // Alone, the row kernel takes the longer requests too: all of them are past
   // max_q_len, and get zeros.

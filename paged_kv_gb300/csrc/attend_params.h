@@ -73,8 +73,9 @@ constexpr int kRowCtasPerSm = 3, kRowWarps = 4;
 inline int row_ctas(int num_sms) { return num_sms * kRowCtasPerSm; }
 inline int row_counters(int num_sms) { return 3 * kRowWarps * row_ctas(num_sms); }
 inline int tile_ctas(int num_sms) { return num_sms; }
-inline size_t counter_bytes(int num_sms) {
-  return (static_cast<size_t>(row_counters(num_sms) + 2 * tile_ctas(num_sms)) * 4 + 255) / 256 * 256;
+constexpr size_t kCounterBytes = PKV_ATTENTION_ZERO_BYTES;  // enough for 431 SMs
+inline bool counters_fit(int num_sms) {
+  return static_cast<size_t>(row_counters(num_sms) + 2 * tile_ctas(num_sms)) * 4 <= kCounterBytes;
 }
 
 // Bytes of the kernels' partial results.

@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -181,9 +182,11 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (cache, device, q, out, lse, cached_len, device_len, table_idx, kv_begin,
-//  max_q_len, page_table, sm_scale, window, status, workspace, stream, cached).
-// With `cached` the workspace is the wrapper's own (or None): where it is too
-// small, -1000 minus the bytes needed comes back and nothing is launched.
+//  max_q_len, page_table, sm_scale, window, status, workspace, stream, default)
+// `default` is None, or the dict of the wrapper's own workspaces, with `workspace`
+// None: by stream and device, each of them large enough for any call.  Where
+// there is none, or the stream is being captured, (bytes needed, the stream's
+// handle, the key, the capture's id or 0) comes back and nothing is launched.
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 17)) return nullptr;
   Args g{a};
@@ -211,18 +214,38 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int window = g.int32(12, "window");
   auto* status = g.flat<int32_t>(13, at::kInt, "status", 1);
   auto* ws = g.flat<uint8_t>(14, at::kByte, "workspace", 0);
-  const bool own = g.int32(16, "cached") != 0;
   const pkv_stream_t s = g.stream(15, device);
   if (g.bad) return nullptr;
   if (b > INT32_MAX) {
     PyErr_SetString(PyExc_ValueError, "cached_len is too long");
     return nullptr;
   }
-  const size_t have = ws != nullptr ? THPVariable_Unpack(a[14]).numel() : 0;
-  if (own) {
-    const size_t need = pkv_paged_attention_workspace_bytes(
-        static_cast<int>(b), q.n, max_q, static_cast<int>(q.heads), c->kv_heads, c->head_dim);
-    if (have < need) return PyLong_FromLongLong(-1000 - static_cast<long long>(need));
+  size_t have = ws != nullptr ? THPVariable_Unpack(a[14]).numel() : 0;
+  if (!g.none(16)) {
+    // (User-space addresses have 48 bits at most.)
+    const unsigned long long handle = reinterpret_cast<uintptr_t>(s);
+    const unsigned long long key = handle << 8 | static_cast<unsigned>(device);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(s), &capture, &id) != cudaSuccess ||
+        capture == cudaStreamCaptureStatusNone)
+      id = 0;
+    PyObject* name = PyLong_FromUnsignedLongLong(key);
+    if (name == nullptr) return nullptr;
+    PyObject* own = id == 0 ? PyDict_GetItemWithError(a[16], name) : nullptr;  // borrowed
+    Py_DECREF(name);
+    if (own == nullptr) {
+      if (PyErr_Occurred()) return nullptr;
+      const size_t need = pkv_paged_attention_workspace_bytes(
+          static_cast<int>(b), q.n, max_q, static_cast<int>(q.heads), c->kv_heads, c->head_dim);
+      return Py_BuildValue("(KKKK)", static_cast<unsigned long long>(need), handle, key, id);
+    }
+    if (!THPVariable_Check(own)) {
+      PyErr_SetString(PyExc_TypeError, "the default workspace is no tensor");
+      return nullptr;
+    }
+    ws = static_cast<uint8_t*>(THPVariable_Unpack(own).data_ptr());
+    have = THPVariable_Unpack(own).numel();
   }
   return PyLong_FromLong(pkv_paged_attention(
       c, q.p, q.token, q.head, static_cast<int>(q.heads), q.dt, q.n, o.p, o.token, o.head, lse,

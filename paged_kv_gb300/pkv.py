@@ -25,6 +25,7 @@ PKV_OK, PKV_EINVAL, PKV_ENOSPC, PKV_ECUDA, PKV_EUNSUPPORTED = 0, -1, -2, -3, -4
 PKV_FP32, PKV_BF16, PKV_FP16 = 0, 1, 2
 PKV_MAX_VOCAB_FP32, PKV_MAX_VOCAB_BF16 = 262144, 524288
 PKV_MAX_HEAD_DIM = 128
+PKV_ATTENTION_ZERO_BYTES = 65536
 ST_NONFINITE, ST_ALL_NEG_INF, ST_ROW_OOB, ST_COL_OOB, ST_BAD_UNIFORM, ST_NOSPC = 1, 2, 4, 8, 16, 32
 ST_TIMEOUT = 64
 ST_TOKEN_CAP = 128
@@ -562,7 +563,42 @@ def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch
     return q_out
 
 
+# Default workspaces, by stream handle and device: made once, never replaced or dropped,
+# so that a call in flight keeps its own.  Those of captures, with the capture's id.
 _attention_workspaces = {}
+_capture_workspaces = {}
+
+
+def _default_attention_workspace(need, handle, key, capture, index) -> torch.Tensor:
+    """The workspace of the calls on one stream, made and zeroed on that stream.
+
+    A stream that is being captured gets one of the capture's: it lies in the graph's
+    memory and each replay zeroes it, so neither other graphs nor calls outside share
+    it.  It is kept for the capture's later calls.
+    """
+    if capture == 0:
+        # The most that any call of this device needs.
+        need = paged_attention_workspace_bytes(1, 64, 64, 1, 1, PKV_MAX_HEAD_DIM)
+    with _lock:
+        if capture == 0:
+            ws = _attention_workspaces.get(key)
+        else:
+            owner, ws = _capture_workspaces.get(key, (0, None))
+            if owner != capture or ws.numel() < need:
+                ws = None
+        if ws is None:
+            device = torch.device("cuda", index)
+            # (1 and 2 name the legacy and the calling thread's default stream.)
+            stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 2
+                      else torch.cuda.default_stream(device))
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+                ws[:PKV_ATTENTION_ZERO_BYTES].zero_()
+            if capture == 0:
+                _attention_workspaces[key] = ws
+            else:
+                _capture_workspaces[key] = (capture, ws)
+    return ws
 
 
 def paged_attention_workspace_bytes(B: int, n_tokens: int, max_q_len: int, q_heads: int,
@@ -582,25 +618,23 @@ def paged_attention(q: torch.Tensor, cache: KVCache, cached_len: torch.Tensor,
     """pkv_paged_attention: causal attention of the packed queries ``q`` [n, q_heads,
     head_dim] (request i's are the positions [cached_len[i], device_len[i])) over
     ``cache``.  ``max_q_len`` bounds a request's query tokens (1 for a decode step);
-    ``sm_scale`` defaults to head_dim ** -0.5.  ``workspace`` (zeroed uint8, one per
-    stream) defaults to a buffer cached per device.  Returns ``out`` (allocated here if
-    not given); ``lse`` [n, q_heads] fp32 receives the log-sum-exp if given.  See
-    include/pkv.h."""
+    ``sm_scale`` defaults to head_dim ** -0.5.  ``workspace`` (uint8, its first
+    PKV_ATTENTION_ZERO_BYTES zeroed once; calls that may overlap pass different ones)
+    defaults to a buffer of the stream's own (some 60 MB, kept), in a capture to one of
+    the capture's.  Returns ``out`` (allocated here if not given); ``lse`` [n, q_heads]
+    fp32 receives the log-sum-exp if given.  See include/pkv.h."""
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    cached = workspace is None
-    if cached:
-        workspace = _attention_workspaces.get(cache._index)
     call = (_binding or _bind()).paged_attention
     rc = call(cache._ref, cache._index, q, out, lse, cached_len, device_len, table_idx, kv_begin,
-              max_q_len, page_table, sm_scale, window, status, workspace, stream, cached)
+              max_q_len, page_table, sm_scale, window, status, workspace, stream,
+              _attention_workspaces if workspace is None else None)
     if rc:
-        if rc < -1000:  # as ``_workspace``: one zero-initialised buffer per device
-            workspace = torch.zeros(-1000 - rc, dtype=torch.uint8, device=cache.device)
-            _attention_workspaces[cache._index] = workspace
+        if rc.__class__ is tuple:  # the stream has no workspace yet
+            workspace = _default_attention_workspace(*rc, cache._index)
             rc = call(cache._ref, cache._index, q, out, lse, cached_len, device_len, table_idx,
                       kv_begin, max_q_len, page_table, sm_scale, window, status, workspace, stream,
-                      False)
+                      None)
         _check(rc)
     return out
 
