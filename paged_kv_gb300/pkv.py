@@ -544,6 +544,25 @@ def _bind():
     return _binding
 
 
+def _torch_stream(stream, device):
+    """A stream object or handle as one of torch's."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream, device)
+    # (1 and 2 name the legacy and the calling thread's default stream.)
+    return (torch.cuda.ExternalStream(handle, device=device) if handle > 2
+            else torch.cuda.default_stream(device))
+
+
+def _new_like(q: torch.Tensor, stream) -> torch.Tensor:
+    """A dense output of ``q``'s shape, in memory of the call's stream: another stream's
+    may still be written there by work that came before."""
+    if stream is None or not q.is_cuda:  # (the binding refuses the latter)
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    with torch.cuda.stream(_torch_stream(stream, q.device)):
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+
+
 def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
               out_loc: torch.Tensor, cos_sin: Optional[torch.Tensor] = None,
               interleaved: bool = False, q: Optional[torch.Tensor] = None,
@@ -555,7 +574,7 @@ def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: torch
     rotation).  Returns the rotated queries (``q_out``, allocated here if not given;
     None without ``q``).  See include/pkv.h."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new_like(q, stream)
     rc = (_binding or _bind()).append_kv(cache._ref, cache._index, k, v, positions, out_loc, cos_sin,
                                          interleaved, q, q_out, total_tokens, status, stream)
     if rc:
@@ -588,10 +607,7 @@ def _default_attention_workspace(need, handle, key, capture, index) -> torch.Ten
                 ws = None
         if ws is None:
             device = torch.device("cuda", index)
-            # (1 and 2 name the legacy and the calling thread's default stream.)
-            stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 2
-                      else torch.cuda.default_stream(device))
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(_torch_stream(handle, device)):
                 ws = torch.empty(need, dtype=torch.uint8, device=device)
                 ws[:PKV_ATTENTION_ZERO_BYTES].zero_()
             if capture == 0:
@@ -624,7 +640,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, cached_len: torch.Tensor,
     the capture's.  Returns ``out`` (allocated here if not given); ``lse`` [n, q_heads]
     fp32 receives the log-sum-exp if given.  See include/pkv.h."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new_like(q, stream)
     call = (_binding or _bind()).paged_attention
     rc = call(cache._ref, cache._index, q, out, lse, cached_len, device_len, table_idx, kv_begin,
               max_q_len, page_table, sm_scale, window, status, workspace, stream,

@@ -143,3 +143,27 @@ def test_a_workspace_needs_no_more_zeros_than_it_says():
     for _ in range(3):
         assert x.good(x(workspace=ws))
     assert not ws[:pkv.PKV_ATTENTION_ZERO_BYTES].any()
+
+
+@pytest.mark.parametrize("how", ["object", "handle"])
+def test_outputs_are_the_call_streams_memory(how):
+    """Memory that the current stream has freed and has yet to write is not taken for the
+    output of a call on another stream."""
+    x = Problem(150, 128, 9)
+    n, hkv, d = 151, 2, 128
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    loc = pos.clone()
+    cache = pkv.KVCache.empty(40, 16, hkv, d)
+    k = torch.zeros(n, hkv, d, dtype=x.q.dtype, device=DEV)
+    side = torch.cuda.Stream()
+    stream = side if how == "object" else side.cuda_stream
+    torch.cuda.synchronize()
+    for call, want in ((lambda: x(stream=stream), x.want),
+                       (lambda: pkv.append_kv(cache, k, k, pos, loc, q=x.q, stream=stream), x.q)):
+        late = torch.empty_like(x.q)
+        torch.cuda._sleep(20_000_000)
+        late.fill_(7.0)
+        del late
+        out = call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
