@@ -15,8 +15,9 @@
 // Per unit, with keys and values as the A operand so that the few rows are the
 // narrow side of the product:
 //   S^T[32 x 8] = K[32 x D] Q^T,   O^T[D x 8] += V^T[D x 32] P^T
-// on mma.m16n8k16 with fp16 inputs: e4m3 codes are exact in fp16, and a query
-// is scaled to at most 2 by a power of two, so the products are exact.  Scores
+// on mma.m16n8k16 with fp16 inputs: e4m3 codes are exact in fp16, and a bf16
+// query row, scaled below 2^15 by a power of two, is too, but for elements below
+// 2^-31 of its largest (which keep an absolute 2^-39 of it).  Scores
 // take the page's key scale in fp32.  Weights carry the page's value scale:
 // p = 2^3 2^(s - m) vs goes to fp16 (11 bits), l sums 2^(s - m) in fp32, so
 // neither over- nor underflows for any scales.  The reference m is not the
@@ -344,7 +345,8 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
     }
     float unit = 1.0f;
     if (P.bf16) {
-      // To fp16 by way of a power of two that puts the row's largest in [1, 2).
+      // To fp16 by way of a power of two that puts the row's largest in [2^14,
+      // 2^15): bf16's 8 bits then fit down to 2^-31 of it.
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i) {
         const float2 x = Pair<T>::unpack(raw[i]);
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-      if (e > 0 && e < 254) unit = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      unit = __uint_as_float(static_cast<uint32_t>(min(268 - e, 254)) << 23);
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i) {
         const float2 x = Pair<T>::unpack(raw[i]);

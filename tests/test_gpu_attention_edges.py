@@ -167,3 +167,39 @@ def test_requests_of_many_rows_past_the_bound_get_zeros(dt, group, new, most):
             assert not got[rows].any() and bool((lse[rows] == -math.inf).all())
         else:
             check({x: y[rows] for x, y in want.items()}, q[rows], got[rows], lse[rows])
+
+
+@pytest.mark.parametrize("small", [2.0 ** -16, 2.0 ** -27], ids=["2^-16", "2^-27"])
+def test_small_query_elements_beside_a_large_one_in_decoding(small):
+    p = ref.page_problem([200, 31], [1, 3], 16, 2, 64, 90)
+    p["k_scale"][:] = 1.0
+    bits = p["k"].float().clone()
+    bits[..., 0] = 0.0
+    p["k"] = bits.to(torch.float8_e4m3fn)
+    g = torch.Generator().manual_seed(91)
+    q = small * (1 + torch.rand(4, 4, 64, generator=g))
+    q = (q * torch.where(torch.rand(q.shape, generator=g) < 0.5, -1.0, 1.0)).to(torch.bfloat16)
+    q[..., 0] = 1.0
+    sm_scale = 5 / (small * 384)
+    want = attend(p, q, sm_scale)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
+    assert status == 0
+    check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 5])
+@pytest.mark.parametrize("power", [-133, -126, -119, -100, 126, 127])
+def test_queries_at_the_ends_of_bf16(new, power):
+    """The largest magnitudes, the smallest and subnormal ones, under a scale that makes
+    their scores ordinary ones."""
+    p = ref.page_problem([150], [new], 16, 1, 64, 92)
+    p["k_scale"][:] = 2.0 ** (-6 if power > 0 else 20)
+    g = torch.Generator().manual_seed(93)
+    q = torch.where(torch.rand(new, 2, 64, generator=g) < 0.5, -1.0, 1.0)
+    q = (q * 2.0 ** max(power, -133)).to(torch.bfloat16)
+    # Scores of some units: 48 * sqrt(64) * |q| * scales.
+    sm_scale = 2.0 ** (-power - 8 + 6) if power > 0 else 2.0 ** min(-power - 8 - 20, 100)
+    want = attend(p, q, sm_scale)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
+    assert status == 0
+    check(want, q, out, lse)
