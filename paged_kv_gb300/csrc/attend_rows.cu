@@ -19,8 +19,11 @@
 // query row, scaled below 2^15 by a power of two, is too, but for elements below
 // 2^-31 of its largest (which keep an absolute 2^-39 of it).  Scores
 // take the page's key scale in fp32.  Weights carry the page's value scale:
-// p = 2^3 2^(s - m) vs goes to fp16 (11 bits), l sums 2^(s - m) in fp32, so
-// neither over- nor underflows for any scales.  The reference m is not the
+// p = 2^-22 2^(s - m) vs goes to fp16 (11 bits), l sums 2^(s - m) in fp32.  m is
+// such that the largest p of the positions that it was taken from is 1.  With
+// that 2^-22, scales of 2^-64 to 2^119 put l's largest terms between 2^-97 and
+// 2^101: neither sums nor weights of 2^-29 of the largest are lost.  The
+// reference m is not the
 // running maximum: it is taken from a row's first positions and moves only
 // where the weights under it sum to more than 2^15.  So a unit needs no maximum
 // over its lanes, and few units rescale.
@@ -69,7 +72,7 @@ constexpr int kLead = 3, kLeast = 2;
 // 14.5 and 14.3 us, long contexts 72, 72 and 78.
 constexpr int kGroup = 16;
 static_assert(kStep == 32, "a lane looks up one position");
-constexpr float kUnit = 8.0f;            // a weight in fp16 is this times 2^(s - m) vs
+constexpr float kUnit = 0x1p-22f;        // a weight in fp16 is this times 2^(s - m) vs
 constexpr float kLimit = 32768.0f;       // sum of such weights that moves m
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
           float t = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 2 * kM; ++i)
-            t = fmaxf(t, s[i >> 1][2 * (i & 1) + c] + lg2(fmaxf(vs[i], 5.42101086e-20f)));
+            t = fmaxf(t, s[i >> 1][2 * (i & 1) + c] + lg2(fmaxf(vs[i], 0x1p-64f * kUnit)));
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
           t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));

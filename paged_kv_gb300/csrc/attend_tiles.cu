@@ -15,10 +15,12 @@
 //     their way to shared memory, P = 2^(s - m) vs in tensor memory, in S's
 //     place, with the page's value scale in it.  l sums 2^(s - m) in fp32.
 // P and V take the queries' type.  bf16 (8 bits) has fp32's range: m is taken
-// from a row's first columns and moves only when weights pass 2^60.  fp16 (11
-// bits) is held below 2^15 with m's weight at 2^3, which keeps 11 bits down to
-// 2^-17 of that and some down to 2^-27.  When m moves, O is rescaled in tensor
-// memory by the row's own thread.
+// from a row's first columns, its weight 2^22, and moves only when weights pass
+// 2^60.  fp16 (11 bits) is held below 2^15 with m's weight at 2^3, which keeps 11
+// bits down to 2^-17 of that and some down to 2^-27.  m lies so (by 2^22) that
+// l's terms of up to 2^22 / vs keep 2^-29 of the largest for a vs of 2^119; terms
+// of small scales may pass 2^100 long before P's do, and move m too.  When m
+// moves, O is rescaled in tensor memory by the row's own thread.
 //
 // Roles (16 warps): warps 0-3 and 4-7 are the softmax of tile 0 and 1, a
 // thread a row; warps 8-11 bring V, converting it in registers; warp 12 issues
@@ -85,14 +87,20 @@ __host__ __device__ constexpr UnitShape unit_shape() {
 }
 
 // P and V are of the queries' type.  An entry of P is `unit` 2^(s - m) vs, and
-// the sum of kPart of them may reach `limit` before m has to move.
+// the sum of kPart of them may reach `limit` before m has to move.  m is the
+// largest s + log2 vs - kRaise; scales below `least` count as that there, so that
+// their terms of l end at 2^22 / least (fp16's P needs all of its range, and its
+// limit bounds l too).
+constexpr float kRaise = 22.0f;
 template <typename W> struct Weight;
 template <> struct Weight<__nv_bfloat16> {
-  static constexpr float unit = 1.0f, limit = 1.152921504606846976e18f;  // 2^60
+  static constexpr float unit = 1.0f, limit = 0x1p60f, least = 0x1p-20f;
+  static constexpr float sum_limit = 0x1p100f;  // of kPart terms of l
   static constexpr int type = 1;
 };
 template <> struct Weight<__half> {
-  static constexpr float unit = 8.0f, limit = 32768.0f;
+  static constexpr float unit = 0x1p-19f, limit = 0x1p15f, least = 0x1p-64f;
+  static constexpr float sum_limit = INFINITY;
   static constexpr int type = 0;
 };
 
@@ -104,7 +112,7 @@ struct Plan {
   static constexpr int q = 0;
   static constexpr int k = q + 2 * NS * kQBytes;
   static constexpr int v = k + kK * kKBytes;
-  static constexpr int sc = v + kV * kVBytes;        // scales, kSc slots: ks, log2 vs, vs
+  static constexpr int sc = v + kV * kVBytes;        // scales, kSc slots: ks, lv, vs (above)
   static constexpr int gr = sc + kSc * 3 * kTile * 4;   // the same of each group of 16
   static constexpr int off = gr + kSc * 8 * 16;         // byte offsets
   static constexpr int bar = off + kSc * kTile * 8;
@@ -331,7 +339,8 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
       if (i == 0 || second) {
         const int tok = tid + i * kPlaceThreads;
         float* at = s_sc + slot * 3 * kTile + tok;
-        const float lv = lg2(fmaxf(v0[i], 5.42101086e-20f)), vw = v0[i] * Weight<T>::unit;  // 2^-64
+        const float lv = lg2(fmaxf(v0[i], Weight<T>::least)) - kRaise;
+        const float vw = v0[i] * Weight<T>::unit;
         at[0] = k0[i];
         at[kTile] = lv;
         at[2 * kTile] = vw;
@@ -600,7 +609,7 @@ __device__ __noinline__ void rescale(uint32_t o_tmem, int d, uint32_t p_tmem, in
   }
 }
 
-// The largest s + log2 vs of kPart columns of a row, of those in [from, to].
+// The largest s + lv of kPart columns of a row, of those in [from, to].
 template <bool GROUPS>
 __device__ __noinline__ float highest(uint32_t s_tmem, const float* sc, const float4* gr, int from,
                                       int to, float factor) {
@@ -675,8 +684,9 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
         sum = g == 0 ? gsum : add2(sum, gsum);
         if (GROUPS) held = fma2(gsum, vg2, held);
       }
-      const float2 h = unpack2(held);
-      const bool past = !(h.x + h.y <= Weight<W>::limit) || m == -INFINITY;
+      const float2 h = unpack2(held), w = unpack2(sum);
+      const bool past = !(h.x + h.y <= Weight<W>::limit) ||
+                        w.x + w.y > Weight<W>::sum_limit || m == -INFINITY;
       if (moved || !__any_sync(kFull, past)) break;
       const float most = highest<GROUPS>(s_tmem + kPart * q, sc, gr, from, to, factor);
       const float now = past ? fmaxf(m, most) : m;

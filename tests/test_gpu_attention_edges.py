@@ -203,3 +203,68 @@ def test_queries_at_the_ends_of_bf16(new, power):
     out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
     assert status == 0
     check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 4, 130])
+@pytest.mark.parametrize("power", [-64, -20, 100, 112, 119])
+def test_value_scales_at_the_ends_of_their_range(new, power):
+    """One position leads by e^8, and thousands of others hold as much together: none of
+    their weights may be lost under any scale."""
+    p = ref.page_problem([3000], [new], 16, 1, 64, 94)
+    p["k_scale"][:] = 1.0
+    p["v_scale"][:] = 2.0 ** power
+    q = queries(new, 1, 64, torch.bfloat16, 95, gain=0.01)
+    q[..., 0] = 1.0
+    code = torch.zeros(3000 + new)
+    code[0] = 64.0
+    set_channel(p, "k", torch.arange(3000 + new), 0, code)
+    want = attend(p, q, 0.125)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=0.125)
+    assert status == 0
+    check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 4, 130])
+@pytest.mark.parametrize("others", [-64, -6])
+def test_scores_that_rise_after_values_of_nothing(dt, new, others):
+    """The first page's values are zeros under the least scale (as pkv_append_kv leaves them);
+    later scores are larger by 2^53 in weight."""
+    p = ref.page_problem([3000], [new], 16, 1, 64, 96)
+    p["k_scale"][:] = 1.0
+    p["v_scale"][:] = 2.0 ** others
+    q = queries(new, 1, 64, dt, 97, gain=0.01)
+    q[..., 0] = 1.03125
+    code = torch.full((3000 + new,), 288.0)
+    code[:32] = 0.0
+    set_channel(p, "k", torch.arange(3000 + new), 0, code)
+    first = p["page_table"][int(p["table_idx"][0]), [0, 16]].long() // 16
+    bits = p["v"].float().clone()
+    bits[first] = 0.0
+    p["v"] = bits.to(torch.float8_e4m3fn)
+    p["v_scale"][first] = 2.0 ** -64
+    want = attend(p, q, 0.125)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=0.125)
+    assert status == 0
+    check(want, q, out, lse)
+
+
+def test_many_scores_that_rise_under_the_least_value_scale():
+    """As above for long ranges: sums of weights that the least scale makes large."""
+    requests, cached, new, hkv = 12, 3000, 130, 8
+    p = ref.page_problem([cached], [new], 16, hkv, 64, 98)
+    p["k_scale"][:] = 1.0
+    p["v_scale"][:] = 2.0 ** -64
+    q = queries(new, hkv, 64, torch.bfloat16, 99, gain=0.0005)
+    q[..., 0] = 1.0546875
+    code = torch.full((cached + new,), 288.0)  # 2^54.8 in weight
+    code[:32] = 0.0
+    set_channel(p, "k", torch.arange(cached + new), 0, code)
+    want = attend(p, q, 0.125)
+    many = dict(p)
+    for name in ("cached_len", "device_len", "table_idx"):
+        many[name] = p[name].repeat(requests)
+    out, lse, status = call(many, make_cache(p), q.repeat(requests, 1, 1), sm_scale=0.125)
+    assert status == 0
+    for i in range(requests):
+        check(want, q, out[i * new:(i + 1) * new], lse[i * new:(i + 1) * new])
