@@ -81,6 +81,9 @@ constexpr int kVBytes = 2 * kVHalf;
 constexpr int kLead = 6;
 constexpr int kPart = 32;                // columns a softmax thread has in registers
 constexpr float kLn2 = 0.693147180559945309f;
+// Least factor of a score whose product with a key scale (2^-64 and more) is
+// normal, and fp32's least normal number, at which smaller products are held.
+constexpr float kLeastFactor = 0x1p-62f, kTiny = 0x1p-126f;
 constexpr int kWaitTries = 1 << 20;
 __host__ __device__ constexpr UnitShape unit_shape() {
   return UnitShape{kBlockRows, kTile, kRowLimit + 1, INT32_MAX, 1, kLead};
@@ -627,14 +630,14 @@ __device__ __noinline__ float highest(uint32_t s_tmem, const float* sc, const fl
 
 // One row's softmax of one unit: reads S, adds to l, leaves P in S's place.
 // Columns outside [from, to] are not seen.  GROUPS: scales are the same over 16
-// columns.  W: P's type.
+// columns.  W: P's type.  TINY: ks * factor may leave fp32's range below.
 //
 // S goes through the registers kPart columns at a time (all 128 would not fit).
 // The reference m is not the running maximum but one from the row's first
 // columns, for as long as the weights under it stay below W's limit; their sum
 // shows that, so no maximum is taken.  Where it is passed, m and what was
 // summed under it move, and the columns are done again.
-template <bool GROUPS, typename W>
+template <bool GROUPS, typename W, bool TINY = false>
 __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
                                                const float4* gr, int from, int to, float factor,
                                                int o_cols, float m, float l) {
@@ -670,6 +673,10 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
             const float2 ks = *reinterpret_cast<const float2*>(sc + col);
             const float2 vs = *reinterpret_cast<const float2*>(sc + 2 * kTile + col);
             f = mul2(pack2(ks.x, ks.y), pack2(factor, factor));
+            if (TINY) {  // (a column that is not seen stays at -inf)
+              const float2 x = unpack2(f);
+              f = pack2(fmaxf(x.x, kTiny), fmaxf(x.y, kTiny));
+            }
             v = pack2(vs.x, vs.y);
           }
           const float2 a = unpack2(
@@ -713,6 +720,13 @@ __device__ __noinline__ float2 softmax_mixed(uint32_t s_tmem, uint32_t o_tmem, c
   return softmax_unit<false, W>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
 }
 
+template <typename W>
+__device__ __noinline__ float2 softmax_tiny(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
+                                            const float4* gr, int from, int to, float factor,
+                                            int o_cols, float m, float l) {
+  return softmax_unit<false, W, true>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
+}
+
 // What a block's units need of one softmax thread.
 struct RowState {
   float m, l;
@@ -722,7 +736,8 @@ struct RowState {
 
 // The softmax of one row over `n` units.
 //   from, to: columns of the first unit that the row sees, going down by kTile
-//   a unit;  tile: bit 0 the tile, bit 1 scales by groups may be used.
+//   a unit;  tile: bit 0 the tile, bit 1 scales by groups may be used, bit 2
+//   some row of the warp has a factor below kLeastFactor.
 template <typename W>
 __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float* s_sc,
                                                const float4* s_gr, uint32_t s_tmem, uint32_t o_tmem,
@@ -739,10 +754,12 @@ __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float*
     const int cols = j > 0 ? d : 0;
     const int* mixed = B->mixed[slot];
     const bool groups = (tile & 2) != 0 && (mixed[0] | mixed[1] | mixed[2]) == 0;
+    const float* sc = s_sc + slot * 3 * kTile;
     const float2 ml =
         groups ? softmax_unit<true, W>(s_tmem, o_tmem, s_sc, gr, from, to, factor, cols, r.m, r.l)
-               : softmax_mixed<W>(s_tmem, o_tmem, s_sc + slot * 3 * kTile, gr, from, to, factor, cols,
-                                  r.m, r.l);
+        : (tile & 4) != 0
+            ? softmax_tiny<W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
+            : softmax_mixed<W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
     r.m = ml.x;
     r.l = ml.y;
     tc::wait_st();
@@ -765,7 +782,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
   const uint32_t s_tmem = lanes + t * kTile, o_tmem = s_tmem + 256;
   const float* s_sc = reinterpret_cast<const float*>(smem + L::sc);
   const float4* s_gr = reinterpret_cast<const float4*>(smem + L::gr);
-  const int tile = t + (P.c.page_size % 16 == 0 ? 2 : 0);
+  const int by_groups = P.c.page_size % 16 == 0 ? 2 : 0;
   RowState st{0.0f, 0.0f, 0u, 0u};
   while (c.left > 0) {
     const int t_begin = c.tile;
@@ -821,10 +838,11 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
         top = max(top & 0xffffu, top >> 16);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-        // To [128, 256) by a power of two.
+        // To [128, 256) by a power of two (2^126 at most).
         const int e = static_cast<int>(__float_as_uint(Pair<T>::unpack(top).x) >> 23);
-        const float unit =
-            e > 8 && e < 255 ? __uint_as_float(static_cast<uint32_t>(261 - e) << 23) : 1.0f;
+        const float unit = top != 0u && e < 255  // (zeros: a row that is not there)
+                               ? __uint_as_float(static_cast<uint32_t>(261 - max(e, 8)) << 23)
+                               : 1.0f;
         const float f = __shfl_sync(kFull, unit, (lane & 1) * 16);  // (and all have read)
         if ((lane >> 1) == i) factor = f;
         // Not all codes have an infinity: a row that is not finite is NaNs (0x7f in
@@ -851,7 +869,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
                 make_uint2((o[0] | (o[1] << 16)) | nans, (o[2] | (o[3] << 16)) | nans);
         }
       }
-      factor = fmaxf(fabsf(P.scale_log2) / factor, 1.17549435e-38f);  // -inf stays -inf
+      factor = fabsf(P.scale_log2) / factor;
       tc::fence_smem();
       tc::fence_before();
       arrive(&B->q_full[t]);
@@ -865,8 +883,9 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       const int base = c.k.start + t_begin * kTile;
       st.m = -INFINITY;
       st.l = 0.0f;
+      const int how = __any_sync(kFull, factor < kLeastFactor) ? 4 : by_groups;
       st = softmax_units<T>(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
-                            tile);
+                            t + how);
     }
     // ---- the block's end: O is complete
     wait(B, &B->s_full[t], st.s_phase);

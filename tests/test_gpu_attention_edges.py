@@ -268,3 +268,24 @@ def test_many_scores_that_rise_under_the_least_value_scale():
     assert status == 0
     for i in range(requests):
         check(want, q, out[i * new:(i + 1) * new], lse[i * new:(i + 1) * new])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 5, 140])
+@pytest.mark.parametrize("sm_scale", [0.0, 2.0 ** -120, -(2.0 ** -60)])
+@pytest.mark.parametrize("ps", [16, 5])
+def test_no_scores_to_speak_of_and_keys_of_nothing(dt, new, sm_scale, ps):
+    """Products that fall below fp32's range, under the least key scale: a plain average of
+    what each row sees, and nothing of what it does not."""
+    p = ref.page_problem([150, 0], [new, 2], ps, 1, 64, 100)
+    p["k_scale"][::2] = 2.0 ** -64
+    q = queries(new + 2, 2, 64, dt, 101)
+    want = attend(p, q, sm_scale)
+    out, lse, status = call(p, make_cache(p), q, sm_scale=sm_scale)
+    assert status == 0
+    check(want, q, out, lse)
+
+
+@pytest.mark.parametrize("power", [-133, -126, -119, -100, 126, 127])
+def test_prompt_queries_at_the_ends_of_bf16(power):
+    test_queries_at_the_ends_of_bf16(140, power)
