@@ -45,8 +45,9 @@
 // reaches; 48 chunks of 1 to 512 tokens over up to 2000: 246 us, 414 TFLOP/s.
 //
 // Every wait ends: after kWaitTries a thread sets `dead`, with which all waits
-// return at once, the loops (whose lengths do not depend on data) run out,
-// tensor memory is freed and PKV_ST_TIMEOUT is set.
+// return at once, the loops (whose lengths do not depend on data) run out, the
+// products in flight are waited for (with a limit), tensor memory is freed and
+// PKV_ST_TIMEOUT is set.
 
 #include <cuda_runtime.h>
 
@@ -125,6 +126,7 @@ struct Plan {
 struct Bars {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], sc_full[4], sc_empty[4];
   uint64_t q_full[2], s_full[2], p_full[2];
+  uint64_t drained;
   uint32_t tmem;
   int dead;
   int last[2];
@@ -132,6 +134,8 @@ struct Bars {
   int mixed[4][3];   // a group of 16 positions spans pages
   int nan;
 };
+
+static_assert(sizeof(Bars) <= 512, "its place in Plan");
 
 // Phase bookkeeping of a ring.
 struct Ring {
@@ -578,6 +582,12 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
       vr.next(L::kV);
       if (more) kr.next(L::kK);
     }
+  }
+  // All that was issued is done before tensor memory is freed, after waits that
+  // ran out too.
+  if (tc::elect()) tc::commit(&B->drained);
+  __syncwarp();
+  for (int i = 0; i < kWaitTries && !mbar_try_wait(&B->drained, 0u); ++i) {
   }
 }
 
@@ -1071,6 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
       mbar_init(&B->s_full[i], 2);
       mbar_init(&B->p_full[i], 4);
     }
+    mbar_init(&B->drained, 1);
     B->dead = 0;
     B->nan = 0;
     fence_mbar_init();
@@ -1088,7 +1099,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
   } else {
     place_role<T, NS>(P, c, smem, B);
   }
-  // Every product has been waited for (by the last block's softmax).
   __syncwarp();
   tc::fence_before();
   __syncthreads();
