@@ -587,8 +587,8 @@ size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_le
  *   int32 rows of ceil(V / 32) words, mask_stride apart, or NULL; status
  *   device int32 or NULL.
  * Errors: PKV_EINVAL (NULL logits or out, one of a group missing, sizes,
- * strides, B outside [0, 65535], pool_cols >= 2^30), PKV_EUNSUPPORTED (V
- * above PKV_MAX_VOCAB_*), PKV_ECUDA.  B == 0 is a no-op.
+ * strides, B outside [0, 65535], pool_cols >= 2^30, n_bias > 2^30),
+ * PKV_EUNSUPPORTED (V above PKV_MAX_VOCAB_*), PKV_ECUDA.  B == 0 is a no-op.
  */
 int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dtype dt, int B, int V,
                       void* out, int64_t out_stride, const int32_t* token_pool,

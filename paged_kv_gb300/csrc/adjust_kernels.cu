@@ -535,8 +535,9 @@ extern "C" int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dty
   if (bias_ptr != nullptr || bias_ids != nullptr || bias_values != nullptr) {
     if (bias_ptr == nullptr || (n_bias > 0 && (bias_ids == nullptr || bias_values == nullptr)))
       return fail(PKV_EINVAL, "bias_ptr, bias_ids and bias_values go together");
-    if (n_bias < 0 || n_bias > INT32_MAX)
-      return fail(PKV_EINVAL, "n_bias=%lld outside [0, 2^31)", (long long)n_bias);
+    // (The kernel's 32-bit indexes go up to kThreads past a list's end.)
+    if (n_bias < 0 || n_bias > (int64_t{1} << 30))
+      return fail(PKV_EINVAL, "n_bias=%lld outside [0, 2^30]", (long long)n_bias);
   }
   if (mask != nullptr && mask_stride < (V + 31) / 32)
     return fail(PKV_EINVAL, "mask_stride=%lld below ceil(V / 32)=%d", (long long)mask_stride,

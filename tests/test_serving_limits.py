@@ -23,3 +23,12 @@ def test_the_largest_attention_workspace():
     for b, n, longest, hq, hkv, d in ((1, 1, 1, 1, 1, 16), (256, 256, 1, 16, 8, 128),
                                       (9, 70000, 4096, 32, 4, 128), (4096, 10 ** 6, 10 ** 6, 64, 1, 96)):
         assert pkv.PKV_ATTENTION_ZERO_BYTES < need(b, n, longest, hq, hkv, d) <= most
+
+
+def test_bias_lists_end_before_32_bits_do():
+    """Threads look 512 entries ahead in 32 bits."""
+    from test_serving_abi import adjust
+
+    for n in ((1 << 30) + 1, (1 << 31) - 1, 1 << 31):
+        assert adjust(nb=n) == pkv.PKV_EINVAL
+        assert "n_bias" in pkv.last_error()
