@@ -570,8 +570,8 @@ size_t pkv_paged_attention_workspace_bytes(int B, int64_t n_tokens, int max_q_le
  * its bits.
  *
  * `out` may be `logits` itself (same stride): then only what changes is
- * written.  Otherwise the two must not overlap, and all B * V of out is
- * written.  Entries of the history outside [0, V) count for nothing; a bias
+ * written.  Otherwise no rows of the two may overlap (they may take turns in
+ * one buffer), and all B * V of out is written.  Entries of the history outside [0, V) count for nothing; a bias
  * whose id lies outside is dropped and PKV_ST_COL_OOB set.  A row whose
  * table_idx lies outside the pool sets PKV_ST_ROW_OOB, one with device_len
  * outside [0, pool_cols] PKV_ST_COL_OOB, and has no history; one whose

@@ -491,6 +491,23 @@ cudaError_t launch_type(const AdjustParams& P, cudaStream_t s) {
   return aligned ? launch<T, Way::kAligned>(P, s) : launch<T, Way::kAnywhere>(P, s);
 }
 
+// Whether a row of x shares bytes with a row of y (rows of one buffer may take
+// turns).  Each side's rows ascend without overlapping one another.
+bool rows_overlap(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int B, int V,
+                  int elt) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t size = static_cast<uintptr_t>(V) * elt;
+  const uintptr_t xs = x_stride * elt, ys = y_stride * elt;
+  if (x0 + (B - 1) * xs + size <= y0 || y0 + (B - 1) * ys + size <= x0) return false;
+  for (int i = 0, j = 0; i < B && j < B;) {
+    const uintptr_t a = x0 + i * xs, b = y0 + j * ys;
+    if (a + size <= b) ++i;
+    else if (b + size <= a) ++j;
+    else return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 }  // namespace pkv
@@ -519,12 +536,8 @@ extern "C" int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dty
   if (out == nullptr) return fail(PKV_EINVAL, "out is NULL");
   if (logits == out && row_stride != out_stride)
     return fail(PKV_EINVAL, "in place the row strides have to be the same");
-  const int elt = dt == PKV_BF16 ? 2 : 4;
-  if (logits != out) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(logits), o = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t an = a + ((B - 1) * row_stride + V) * elt, on = o + ((B - 1) * out_stride + V) * elt;
-    if (a < on && o < an) return fail(PKV_EINVAL, "logits and out overlap without being the same");
-  }
+  if (logits != out && rows_overlap(logits, row_stride, out, out_stride, B, V, dt == PKV_BF16 ? 2 : 4))
+    return fail(PKV_EINVAL, "logits and out overlap without being the same");
   if (token_pool != nullptr || table_idx != nullptr || prompt_len != nullptr || device_len != nullptr) {
     if (token_pool == nullptr || table_idx == nullptr || prompt_len == nullptr || device_len == nullptr)
       return fail(PKV_EINVAL, "token_pool, table_idx, prompt_len and device_len go together");
