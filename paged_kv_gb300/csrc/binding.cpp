@@ -17,10 +17,12 @@
 
 namespace {
 
-// What a function unpacks; `bad` once an exception is set.
+// What a function unpacks; `bad` once an exception is set.  Every tensor has to be
+// on GPU `device`, once that is known.
 struct Args {
   PyObject* const* a;
   bool bad = false;
+  int device = -1;
 
   template <typename... X>
   void fail(PyObject* type, const char* fmt, X... x) {
@@ -36,6 +38,11 @@ struct Args {
     const at::Tensor& t = THPVariable_Unpack(a[i]);
     if (!t.is_cuda()) {
       fail(PyExc_TypeError, "%s must be a CUDA tensor", name);
+      return nullptr;
+    }
+    if (device >= 0 && t.get_device() != device) {
+      fail(PyExc_ValueError, "%s is on cuda:%d, not on cuda:%d", name,
+           static_cast<int>(t.get_device()), device);
       return nullptr;
     }
     return &t;
@@ -120,7 +127,7 @@ struct Args {
     return static_cast<int>(x);
   }
   // A stream object, an integer handle, or None for the device's current one.
-  pkv_stream_t stream(int i, int device) {
+  pkv_stream_t stream(int i) {
     if (bad) return nullptr;
     if (none(i))
       return reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
@@ -153,7 +160,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Args g{a};
   const pkv_kv_cache* c = g.cache(0);
   if (c == nullptr) return nullptr;
-  const int device = g.int32(1, "device");
+  g.device = g.int32(1, "device");
   const auto k = g.rows(2, "k", -1, c->kv_heads, c->head_dim);
   const auto v = g.rows(3, "v", k.n, c->kv_heads, c->head_dim);
   const auto* pos = g.flat<int32_t>(4, at::kInt, "positions", k.n);
@@ -173,7 +180,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!g.bad && v.dt != k.dt) g.fail(PyExc_TypeError, "v must have k's dtype");
   const auto* total = g.flat<int64_t>(10, at::kLong, "total_tokens", 1);
   auto* status = g.flat<int32_t>(11, at::kInt, "status", 1);
-  const pkv_stream_t s = g.stream(12, device);
+  const pkv_stream_t s = g.stream(12);
   if (g.bad) return nullptr;
   return PyLong_FromLong(pkv_append_kv(
       c, k.p, k.token, k.head, v.p, v.token, v.head, k.dt, k.n, total, pos, loc, cs, max_pos,
@@ -192,7 +199,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Args g{a};
   const pkv_kv_cache* c = g.cache(0);
   if (c == nullptr) return nullptr;
-  const int device = g.int32(1, "device");
+  g.device = g.int32(1, "device");
   const auto q = g.rows(2, "q", -1, -1, c->head_dim);
   const auto o = g.rows(3, "out", q.n, q.heads, c->head_dim);
   if (!g.bad && o.dt != q.dt) g.fail(PyExc_TypeError, "out must have q's dtype");
@@ -214,7 +221,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int window = g.int32(12, "window");
   auto* status = g.flat<int32_t>(13, at::kInt, "status", 1);
   auto* ws = g.flat<uint8_t>(14, at::kByte, "workspace", 0);
-  const pkv_stream_t s = g.stream(15, device);
+  const pkv_stream_t s = g.stream(15);
   if (g.bad) return nullptr;
   if (b > INT32_MAX) {
     PyErr_SetString(PyExc_ValueError, "cached_len is too long");
@@ -224,7 +231,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!g.none(16)) {
     // (User-space addresses have 48 bits at most.)
     const unsigned long long handle = reinterpret_cast<uintptr_t>(s);
-    const unsigned long long key = handle << 8 | static_cast<unsigned>(device);
+    const unsigned long long key = handle << 8 | static_cast<unsigned>(g.device);
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(s), &capture, &id) != cudaSuccess ||
@@ -271,12 +278,13 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  c10::toString(x->scalar_type()));
     return nullptr;
   }
+  g.device = static_cast<int>(x->get_device());
   const int64_t b = x->size(0), v = x->size(1);
   const at::Tensor* o = THPVariable_Check(a[1]) ? &THPVariable_Unpack(a[1]) : nullptr;
-  if (o == nullptr || !o->is_cuda() || o->scalar_type() != x->scalar_type() || o->dim() != 2 ||
-      o->size(0) != b || o->size(1) != v || (o->stride(1) != 1 && v > 1)) {
+  if (o == nullptr || !o->is_cuda() || o->get_device() != g.device ||
+      o->scalar_type() != x->scalar_type() || o->dim() != 2 || o->size(0) != b || o->size(1) != v || (o->stride(1) != 1 && v > 1)) {
     PyErr_SetString(PyExc_ValueError,
-                    "out must be a CUDA tensor of the logits' shape and dtype with unit column stride");
+                    "out must be a tensor of the logits' GPU, shape and dtype with unit column stride");
     return nullptr;
   }
   int64_t pr, pc;
@@ -305,7 +313,7 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   auto* status = g.flat<int32_t>(13, at::kInt, "status", 1);
-  const pkv_stream_t s = g.stream(14, x->get_device());
+  const pkv_stream_t s = g.stream(14);
   if (g.bad) return nullptr;
   if (b > INT32_MAX || v > INT32_MAX) {
     PyErr_SetString(PyExc_ValueError, "logits are too large");
