@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-      unit = __uint_as_float(static_cast<uint32_t>(min(268 - e, 254)) << 23);
+      unit = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i) {
         const float2 x = Pair<T>::unpack(raw[i]);
@@ -371,7 +371,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm) attend_rows_kernel
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int r = 2 * col_lane + c;
-      cf[c] = P.scale_log2 / __shfl_sync(kFull, unit, (2 * col_lane + c) * 4);
+      // (1 / unit by its exponent: a division takes its slow way for the large
+      // units of rows that are not there.)
+      cf[c] = P.scale_log2 * __uint_as_float(
+          0x7f000000u - __float_as_uint(__shfl_sync(kFull, unit, (2 * col_lane + c) * 4)));
       const int p = cu.r.cached + (cu.k.row0 + r) / P.group;
       // (A row that is not there sees everything: it must not keep m waiting.)
       hi[c] = r < cu.k.rows ? min(p, cu.k.end - 1) : INT32_MAX;

@@ -282,7 +282,8 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t b = x->size(0), v = x->size(1);
   const at::Tensor* o = THPVariable_Check(a[1]) ? &THPVariable_Unpack(a[1]) : nullptr;
   if (o == nullptr || !o->is_cuda() || o->get_device() != g.device ||
-      o->scalar_type() != x->scalar_type() || o->dim() != 2 || o->size(0) != b || o->size(1) != v || (o->stride(1) != 1 && v > 1)) {
+      o->scalar_type() != x->scalar_type() || o->dim() != 2 || o->size(0) != b ||
+      o->size(1) != v || (o->stride(1) != 1 && v > 1)) {
     PyErr_SetString(PyExc_ValueError,
                     "out must be a tensor of the logits' GPU, shape and dtype with unit column stride");
     return nullptr;
