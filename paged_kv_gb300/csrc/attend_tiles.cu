@@ -92,19 +92,16 @@ __host__ __device__ constexpr UnitShape unit_shape() {
 
 // P and V are of the queries' type.  An entry of P is `unit` 2^(s - m) vs, and
 // the sum of kPart of them may reach `limit` before m has to move.  m is the
-// largest s + log2 vs - kRaise; scales below `least` count as that there, so that
-// their terms of l end at 2^22 / least (fp16's P needs all of its range, and its
-// limit bounds l too).
-constexpr float kRaise = 22.0f;
+// largest s + log2 vs - kRaise.  A unit adds up to 2^126 to l in bf16 (fp16's
+// limit keeps it below 2^100): where l passes kSumLimit, m goes up by kStep.
+constexpr float kRaise = 22.0f, kSumLimit = 0x1p100f, kStep = 64.0f;
 template <typename W> struct Weight;
 template <> struct Weight<__nv_bfloat16> {
-  static constexpr float unit = 1.0f, limit = 0x1p60f, least = 0x1p-20f;
-  static constexpr float sum_limit = 0x1p100f;  // of kPart terms of l
+  static constexpr float unit = 1.0f, limit = 0x1p60f;
   static constexpr int type = 1;
 };
 template <> struct Weight<__half> {
-  static constexpr float unit = 0x1p-19f, limit = 0x1p15f, least = 0x1p-64f;
-  static constexpr float sum_limit = INFINITY;
+  static constexpr float unit = 0x1p-19f, limit = 0x1p15f;
   static constexpr int type = 0;
 };
 
@@ -126,13 +123,13 @@ struct Plan {
 struct Bars {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], sc_full[4], sc_empty[4];
   uint64_t q_full[2], s_full[2], p_full[2];
-  uint64_t drained;
   uint32_t tmem;
   int dead;
   int last[2];
   int partial[4];
   int mixed[4][3];   // a group of 16 positions spans pages
   int nan;
+  uint64_t drained;
 };
 
 static_assert(sizeof(Bars) <= 512, "its place in Plan");
@@ -346,7 +343,7 @@ __device__ __noinline__ void place_role(const AttendParams& P, Cursor a, uint8_t
       if (i == 0 || second) {
         const int tok = tid + i * kPlaceThreads;
         float* at = s_sc + slot * 3 * kTile + tok;
-        const float lv = lg2(fmaxf(v0[i], Weight<T>::least)) - kRaise;
+        const float lv = lg2(fmaxf(v0[i], 0x1p-64f)) - kRaise;
         const float vw = v0[i] * Weight<T>::unit;
         at[0] = k0[i];
         at[kTile] = lv;
@@ -583,8 +580,11 @@ __device__ __noinline__ void mma_role(const AttendParams& P, Cursor c, uint8_t* 
       if (more) kr.next(L::kK);
     }
   }
-  // All that was issued is done before tensor memory is freed, after waits that
-  // ran out too.
+}
+
+// Waits until all products that the warp has issued are done: before tensor
+// memory is freed, after waits that ran out too.
+__device__ __noinline__ void drain(Bars* B) {
   if (tc::elect()) tc::commit(&B->drained);
   __syncwarp();
   for (int i = 0; i < kWaitTries && !mbar_try_wait(&B->drained, 0u); ++i) {
@@ -701,9 +701,8 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
         sum = g == 0 ? gsum : add2(sum, gsum);
         if (GROUPS) held = fma2(gsum, vg2, held);
       }
-      const float2 h = unpack2(held), w = unpack2(sum);
-      const bool past = !(h.x + h.y <= Weight<W>::limit) ||
-                        w.x + w.y > Weight<W>::sum_limit || m == -INFINITY;
+      const float2 h = unpack2(held);
+      const bool past = !(h.x + h.y <= Weight<W>::limit) || m == -INFINITY;
       if (moved || !__any_sync(kFull, past)) break;
       const float most = highest<GROUPS>(s_tmem + kPart * q, sc, gr, from, to, factor);
       const float now = past ? fmaxf(m, most) : m;
@@ -720,6 +719,15 @@ __device__ __forceinline__ float2 softmax_unit(uint32_t s_tmem, uint32_t o_tmem,
     sc += kPart;
     from -= kPart, to -= kPart;
   }
+  if (Weight<W>::type == 1) {
+    const bool past = l > kSumLimit;
+    if (__any_sync(kFull, past)) {
+      const float f = past ? 0x1p-64f : 1.0f;
+      if (past) m += kStep;
+      l *= f;
+      rescale<W>(o_tmem, o_cols, s_tmem, kTile / 2, f);
+    }
+  }
   return make_float2(m, l);
 }
 
@@ -727,14 +735,9 @@ template <typename W>
 __device__ __noinline__ float2 softmax_mixed(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
                                              const float4* gr, int from, int to, float factor,
                                              int o_cols, float m, float l) {
+  if (__any_sync(kFull, factor < kLeastFactor))
+    return softmax_unit<false, W, true>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
   return softmax_unit<false, W>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
-}
-
-template <typename W>
-__device__ __noinline__ float2 softmax_tiny(uint32_t s_tmem, uint32_t o_tmem, const float* sc,
-                                            const float4* gr, int from, int to, float factor,
-                                            int o_cols, float m, float l) {
-  return softmax_unit<false, W, true>(s_tmem, o_tmem, sc, gr, from, to, factor, o_cols, m, l);
 }
 
 // What a block's units need of one softmax thread.
@@ -746,8 +749,7 @@ struct RowState {
 
 // The softmax of one row over `n` units.
 //   from, to: columns of the first unit that the row sees, going down by kTile
-//   a unit;  tile: bit 0 the tile, bit 1 scales by groups may be used, bit 2
-//   some row of the warp has a factor below kLeastFactor.
+//   a unit;  tile: bit 0 the tile, bit 1 scales by groups may be used.
 template <typename W>
 __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float* s_sc,
                                                const float4* s_gr, uint32_t s_tmem, uint32_t o_tmem,
@@ -764,12 +766,10 @@ __device__ __noinline__ RowState softmax_units(RowState r, Bars* B, const float*
     const int cols = j > 0 ? d : 0;
     const int* mixed = B->mixed[slot];
     const bool groups = (tile & 2) != 0 && (mixed[0] | mixed[1] | mixed[2]) == 0;
-    const float* sc = s_sc + slot * 3 * kTile;
     const float2 ml =
         groups ? softmax_unit<true, W>(s_tmem, o_tmem, s_sc, gr, from, to, factor, cols, r.m, r.l)
-        : (tile & 4) != 0
-            ? softmax_tiny<W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l)
-            : softmax_mixed<W>(s_tmem, o_tmem, sc, gr, from, to, factor, cols, r.m, r.l);
+               : softmax_mixed<W>(s_tmem, o_tmem, s_sc + slot * 3 * kTile, gr, from, to, factor, cols,
+                                  r.m, r.l);
     r.m = ml.x;
     r.l = ml.y;
     tc::wait_st();
@@ -893,7 +893,7 @@ __device__ __noinline__ void softmax_role(const AttendParams& P, Cursor c, const
       const int base = c.k.start + t_begin * kTile;
       st.m = -INFINITY;
       st.l = 0.0f;
-      const int how = __any_sync(kFull, factor < kLeastFactor) ? 4 : by_groups;
+      const int how = __any_sync(kFull, factor < kLeastFactor) ? 0 : by_groups;
       st = softmax_units<T>(st, B, s_sc, s_gr, s_tmem, o_tmem, factor, d, n, lo - base, hi - base,
                             t + how);
     }
@@ -1096,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(
     value_role<T, NS>(P, static_cast<int>(c.left), smem, B);
   } else if (warp == 12) {
     mma_role<T, NS>(P, c, smem, B);
+    drain(B);
   } else {
     place_role<T, NS>(P, c, smem, B);
   }
