@@ -7,12 +7,13 @@ into one shared library against the shared CUDA runtime.  The binding
 (``csrc/binding.cpp``, plain C++ against the installed torch's headers) is
 compiled beside them and linked against that library.  Objects go to
 ``paged_kv_gb300/_build/`` (git-ignored); both are rebuilt only when a source or
-header is newer than them.
+header is newer than them, or when the binding was made for another torch or Python.
 """
 
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -27,6 +28,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")  # the torch that it was made for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -51,6 +53,11 @@ def _torch_dir() -> str:
     return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
 
 
+def _binding_for() -> str:
+    """What the binding's C++ interface depends on."""
+    return "\n".join((_torch_dir(), importlib.metadata.version("torch"), sys.version))
+
+
 def _run(cmd, what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -72,8 +79,11 @@ def _deps():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    if not all(os.path.exists(f) for f in (LIB, BINDING, BINDING_FOR)):
         return True
+    with open(BINDING_FOR) as f:
+        if f.read() != _binding_for():
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _deps())
 
@@ -129,6 +139,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
           "-ltorch_cpu", "-ltorch_python", "-L" + libdir, "-lcudart", "-Wl,-rpath,$ORIGIN",
           "-Wl,-rpath," + torch_lib, "-Wl,-rpath," + libdir], "the binding's link", verbose)
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_for())
     return LIB
 
 
