@@ -513,8 +513,9 @@ int pkv_append_kv(const pkv_kv_cache* cache, const void* k, int64_t k_token_stri
  * lies in places that a query does not see never reaches it.  The softmax
  * runs in fp32; products are of the query (an element far below its row's
  * largest keeps at least an absolute 2^-21 of that), the codes and weights of
- * at least 8 significant bits, accumulated in fp32.  Sums are joined in a fixed
- * order: equal calls give equal bits.
+ * at least 8 significant bits (or an absolute 2^-25 of the row's largest one),
+ * accumulated in fp32.  Sums are joined in a fixed order: equal calls give
+ * equal bits.
  *
  * max_q_len is the host's bound on a request's query tokens.  A request with
  * more sets PKV_ST_TOKEN_CAP; one with a table row outside the table sets

@@ -17,25 +17,28 @@
 //   S^T[32 x 8] = K[32 x D] Q^T,   O^T[D x 8] += V^T[D x 32] P^T
 // on mma.m16n8k16 with fp16 inputs: e4m3 codes are exact in fp16, and a bf16
 // query row, scaled below 2^15 by a power of two, is too, but for elements below
-// 2^-31 of its largest (which keep an absolute 2^-39 of it).  Scores
-// take the page's key scale in fp32.  Weights carry the page's value scale:
+// 2^-31 of its largest (which keep an absolute 2^-39 of it).  Scores take the
+// page's key scale in fp32.  Weights carry the page's value scale:
 // p = 2^-22 2^(s - m) vs goes to fp16 (11 bits), l sums 2^(s - m) in fp32.  m is
-// such that the largest p of the positions that it was taken from is 1.  With
-// that 2^-22, scales of 2^-64 to 2^119 put l's largest terms between 2^-97 and
-// 2^101: neither sums nor weights of 2^-29 of the largest are lost.  The
-// reference m is not the
-// running maximum: it is taken from a row's first positions and moves only
-// where the weights under it sum to more than 2^15.  So a unit needs no maximum
-// over its lanes, and few units rescale.
+// such that the largest p of the positions that it was taken from is 1: p keeps
+// 11 bits down to 2^-14 of that and some down to 2^-24.  With that 2^-22, scales
+// of 2^-64 to 2^119 put l's largest terms between 2^-97 and 2^101: neither sums
+// nor terms of 2^-29 of the largest are lost.  The reference m is not the running
+// maximum: it is taken from a row's first positions and moves only where the
+// weights under it sum to more than 2^15.  So a unit needs no maximum over its
+// lanes, and few units rescale.
 //
-// Bound: bytes.  Each cached byte is read once (2 D per position and head), and
-// close behind the issue of 716 instructions a unit (half of them conversions
-// of codes and their addresses).  256 requests of up to 2513 positions, 16 query
-// and 8 cache heads of 128, pages of 16, bf16: 132 us, 5.2 TB/s; 16 of up to
-// 36864, 32 and 4 heads, pages of 64, fp16: 73 us, 4.0 TB/s; 61 of up to 2006
-// under a window of 777 with 1 to 5 new tokens, 12 heads of 64, pages of 1: 32
-// us (scattered rows of 64 bytes); one of 701: 14.5 us, of which the joins 5 and
-// the rest the start's chain of loads (lengths, places, rows).
+// Bound: for up to 8 rows a cache head each cached byte is read once (2 D per
+// position and head), for more once for every 8 rows.  A warp copies its next
+// unit only when the present one is done (the ring's other slot is free by then,
+// not before): memory waits on its 716 instructions a unit (half of them
+// conversions of codes and their addresses) and they on memory, with 12 warps an
+// SM to hide it.  256 requests of up to 2513 positions, 16 query and 8 cache heads
+// of 128, pages of 16, bf16: 133 us, 5.2 TB/s; 16 of up to 36864, 32 and 4 heads,
+// pages of 64, fp16: 74 us, 4.0 TB/s; 61 of up to 2006 under a window of 777 with
+// 1 to 5 new tokens, 12 heads of 64, pages of 1: 34 us (scattered rows of 64
+// bytes); one of 701: 16.4 us, of which the joins 5 and the rest the start's chain
+// of loads (lengths, places, rows).
 // Blocks of 16 rows, which read the cache half as often but spill and leave one
 // row in two idle where there are 8: 256 requests of 16 rows 292 us against 258
 // (of 32: 538 against 479), 16 long ones of 16 rows 143 against 113.
@@ -60,7 +63,7 @@ namespace {
 constexpr int kWarps = kRowWarps;
 constexpr int kRows = 8;                 // of a block: the narrow side of the products
 constexpr int kStep = 32;                // positions a warp takes at a time: one a lane
-constexpr int kStages = 2;               // ring slots of a warp
+constexpr int kStages = 2;               // ring slots of a warp: kStages - 1 units under way
 constexpr int kLook = 4;                 // units whose places are read at once (1: 149 us for the
                                          // 256 requests against 145, 8: 154)
 // Cost of a block's start in units, and the least cost of a warp's range.  256

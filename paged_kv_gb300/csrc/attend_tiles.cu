@@ -20,7 +20,10 @@
 // bits down to 2^-17 of that and some down to 2^-27.  m lies so (by 2^22) that
 // l's terms of up to 2^22 / vs keep 2^-29 of the largest for a vs of 2^119; terms
 // of small scales may pass 2^100 long before P's do, and move m too.  When m
-// moves, O is rescaled in tensor memory by the row's own thread.
+// moves, O is rescaled in tensor memory by the row's own thread.  bf16 calls with
+// weights in fp16 move m often: 2 x 4096 tokens take 546 us with them instead of
+// 433, 48 short chunks 285 instead of 249.  (With bf16 weights the error against
+// 64 bits is 0.0023; rounding the results to bf16 alone makes 0.0017.)
 //
 // Roles (16 warps): warps 0-3 and 4-7 are the softmax of tile 0 and 1, a
 // thread a row; warps 8-11 bring V, converting it in registers; warp 12 issues
@@ -37,12 +40,13 @@
 // whole rows, a half warp each: this code runs once in 10 to 50 units, and its
 // fetch is what it costs (unrolled it is slower).
 //
-// Bound: neither the tensor pipe (2048 clocks a unit) nor the exponentials
-// (1024), but the chain S -> softmax -> P V of each tile and its barriers: a
-// unit takes 3800 to 4200 clocks with both tiles in turn, and a block's change
-// about 20000.  2 x 4096 tokens over 4096 cached, 16 query and 8 cache heads of
-// 128, bf16: 430 us, 960 TFLOP/s, half of what a library product of that size
-// reaches; 48 chunks of 1 to 512 tokens over up to 2000: 246 us, 414 TFLOP/s.
+// Bound: neither the tensor pipe (2048 clocks a unit, 41 % busy) nor the
+// exponentials (1024), but the chain S -> softmax -> P V of each tile, whose links
+// wait for one another: a unit takes 3800 to 4200 clocks with both tiles in turn,
+// and a block's change about 20000.  2 x 4096 tokens over 4096 cached, 16 query
+// and 8 cache heads of 128, bf16: 433 us, 951 TFLOP/s, half of what a library
+// product of that size reaches; 48 chunks of 1 to 512 tokens over up to 2000: 249
+// us, 410 TFLOP/s.
 //
 // Every wait ends: after kWaitTries a thread sets `dead`, with which all waits
 // return at once, the loops (whose lengths do not depend on data) run out, the
