@@ -515,7 +515,8 @@ int pkv_append_kv(const pkv_kv_cache* cache, const void* k, int64_t k_token_stri
  * largest keeps at least an absolute 2^-21 of that), the codes and weights of
  * at least 8 significant bits (or an absolute 2^-25 of the row's largest one),
  * accumulated in fp32.  Sums are joined in a fixed order: equal calls give
- * equal bits.
+ * equal bits.  |s_t| has to stay below 2^27, beyond which fp32 tells scores
+ * apart by 16 and more and weights may come out as zeros, infinities or NaN.
  *
  * max_q_len is the host's bound on a request's query tokens.  A request with
  * more sets PKV_ST_TOKEN_CAP; one with a table row outside the table sets
