@@ -360,19 +360,25 @@ __device__ float nth_bound(Shared& S, const float* t, int count, uint32_t n, flo
   }));
 }
 
-// Sum of exp(x - m) over a row to some 2^-36: all threads, each of which gets it.
+// Sum of exp(x - m) over a row to some 2^-36: all threads, each of which gets it.  An
+// element's place in the row alone says when it is added: rows of equal logits have equal
+// sums wherever they begin.
 template <typename T>
 __device__ FF exact_sum(const BeamParams& P, Shared& S, int row, float m) {
-  constexpr int kPer = Elements<T>::kPer;
+  constexpr int kAhead = 8;  // elements of a thread whose loads are on their way together
   const int tid = threadIdx.x;
-  const Row<T> r = row_of<T>(P, row);
+  const T* logits = static_cast<const T*>(P.logits) + static_cast<int64_t>(row) * P.row_stride;
   FF s = {0.0f, 0.0f};
 #pragma unroll 1
-  for (int k = tid; k < r.vectors; k += kThreads) {
-    float x[kPer];
-    unpack_row<T>(r, P.V, k, load_vector(r, k), -1, x);
+  for (int v0 = tid; v0 < P.V; v0 += kThreads * kAhead) {
+    float x[kAhead];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) s = add(s, exp_below(x[e], m));
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = v0 + i * kThreads;
+      x[i] = v < P.V ? static_cast<float>(logits[v]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) s = add(s, exp_below(x[i], m));
   }
   s = warp_sum(s);
   __syncthreads();

@@ -1,0 +1,74 @@
+"""pkv.beam_select's order where sums' roundings could change it: equal beams at any place in
+memory."""
+
+import math
+
+import pytest
+import torch
+
+import branch_reference as ref
+from paged_kv_gb300 import pkv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, FP32 = torch.bfloat16, torch.float32
+# A log-sum-exp is off by less than 3e-6, a sum of two fp32 values by some 2^-46 of the largest
+# term, and a score is rounded once.
+ERR, PAIR, STEP = 3e-6, 2.0 ** -44, 2.0 ** -24
+
+
+def select(x, scores, n, eos=-1):
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = pkv.beam_select(x, scores.to(DEV), n, eos=eos, status=st)
+    assert int(st) == 0
+    return got
+
+
+def check(x, gpu, scores, n, want=None, eos=-1):
+    want = ref.beam_select(x, scores, n, eos) if want is None else want
+    got = select(gpu, scores, n, eos)
+    assert torch.equal(got[0].cpu(), want[0])
+    assert torch.equal(got[1].cpu(), want[1])
+    y, z = got[2].cpu().double(), want[2]
+    assert torch.equal(y == -math.inf, z == -math.inf)
+    fine = z > -math.inf
+    tol = ERR + PAIR * scores.double().abs().max() + STEP * z.abs()
+    assert bool(((y - z).abs() <= tol)[fine].all())
+    if eos >= 0:
+        assert torch.equal(got[3].cpu() == -math.inf, want[3] == -math.inf)
+
+
+# ------------------------------------------------------------------ equal beams
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+def test_equal_beams_wherever_their_rows_begin(dt):
+    """Four beams of one request with the same logits and scores: rows of odd sizes one after
+    another begin at different distances from a 16-byte boundary."""
+    g = torch.Generator().manual_seed(1)
+    per = 8 if dt == BF16 else 4
+    for trial in range(24):
+        v = int(torch.randint(9000, 30000, (1,), generator=g)) | 1
+        row = (torch.randn(v, generator=g) * 3).to(dt)
+        scores = -torch.rand(1, 1, generator=g).expand(1, per).contiguous() * 5
+        x = row.repeat(per, 1)
+        lead = trial % per
+        buf = torch.zeros(lead + per * v, dtype=dt, device=DEV)
+        gpu = buf[lead:].view(per, v)
+        gpu.copy_(x)
+        check(x, gpu, scores, per + 1, eos=int(row.argmax()))
+        check(x, gpu, scores, 3)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+def test_flat_equal_beams_wherever_their_rows_begin(dt):
+    """The same where more candidates are equal than the list holds."""
+    g = torch.Generator().manual_seed(2)
+    per = 8 if dt == BF16 else 4
+    for trial in range(12):
+        v = int(torch.randint(5000, 20000, (1,), generator=g)) | 1
+        row = (torch.randn(v, generator=g) * 2).to(dt)
+        row[torch.randperm(v, generator=g)[:1500]] = 9.0
+        x = row.repeat(per, 1)
+        scores = -torch.rand(1, 1, generator=g).expand(1, per).contiguous() * 5
+        check(x, x.to(DEV), scores, 2 * per, eos=int(row.argmax()))
