@@ -298,8 +298,8 @@ struct Shared {
   uint32_t count, hits, flag;
   unsigned long long near;
 };
-// After it in shared memory: each slice's largest t, then the list of those above
-// the threshold.
+// After it in shared memory: each slice's largest t, bounded from below, then the list of
+// those that may reach the threshold.
 size_t finish_bytes(int pairs) { return sizeof(Shared) + static_cast<size_t>(pairs) * 4 + (pairs + 1) / 2 * 4; }
 
 __device__ __forceinline__ int beam_of(uint32_t id) { return (id >> 20) & (PKV_MAX_BEAMS - 1); }
@@ -307,6 +307,19 @@ __device__ __forceinline__ int token_of(uint32_t id) { return id & 0xfffffu; }
 
 __device__ __forceinline__ FF total(const Shared& S, int w, float x) {
   return add(S.off[w], two_sum(x, -S.m[w]));
+}
+
+// t as fp32 computes it is off.h + (x - m).  It is off by the sums' error, off's lower half
+// and three roundings, together at most kNear + 2^-23 (|off| + |t|): where a score cancels a
+// gap of the logits, t is small and its error is not.  This is at least that, with room for
+// the roundings of a bound that is formed with it.
+__device__ __forceinline__ float slack(float off, float t) {
+  return kNear + 0x1p-22f * (fabsf(off) + fabsf(t));
+}
+// Lower bound of a candidate's t, -inf for none.
+__device__ __forceinline__ float at_least(float off, float above) {
+  const float t = off + above;
+  return t - slack(off, t);
 }
 
 // A lower bound of the n-th largest of t[0 .. count), -inf if fewer are above that;
@@ -352,7 +365,11 @@ __device__ float nth_bound(Shared& S, const float* t, int count, uint32_t n, flo
   __syncthreads();
   const int bin = static_cast<int>(S.nth.prefix);
   __syncthreads();
-  if (bin < kBins - 1) return best - (bin + 1) * (1.0f / kBinsPerNat);
+  if (bin < kBins - 1) {
+    // (best - t, below 64, and this difference are rounded.)
+    const float low = best - (bin + 1) * (1.0f / kBinsPerNat);
+    return low - fabsf(low) * 0x1p-22f - 0x1p-18f;
+  }
   // Further away than the bins reach.
   uint32_t ignore;
   return key_float(nth_key<kThreads, 2>(S.nth, n, &ignore, [&](auto&& f) {
@@ -549,7 +566,8 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
       if (i * 32 + lane < C)
-        tops[w * C + i * 32 + lane] = live && part[i].z >= m - kFar ? off.h + (part[i].z - m) : -INFINITY;
+        tops[w * C + i * 32 + lane] =
+            live && part[i].z >= m - kFar ? at_least(off.h, part[i].z - m) : -INFINITY;
     if (lane == 0) {
       S.m[w] = m;
       S.x_end[w] = x_end;
@@ -572,12 +590,15 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
   // ---- a threshold that n_out candidates reach, the endings apart
   uint32_t have;
   float least = nth_bound(S, tops, pairs, n_out, best, &have);
-  auto add_hits = [&](float t) {  // a little lower: errors of the sums, roundings of t
-    const float low = t - 4.0f * kNear - fabsf(t) * 0x1p-21f;
-    if (tid < W)
-      S.xmin[tid] = fmaxf(S.m[tid] - kFar, __fadd_rd(low - S.off[tid].h, S.m[tid]));
+  auto add_hits = [&](float t) {
+    if (tid < W) {
+      const float off = S.off[tid].h, x = t - off;
+      S.xmin[tid] = fmaxf(S.m[tid] - kFar, __fadd_rd(__fsub_rd(x, slack(off, x)), S.m[tid]));
+    }
+    // (From a slice's lower bound up to its upper one: twice its slack.)
     for (int i = tid; i < pairs; i += kThreads)
-      if (tops[i] > -INFINITY && tops[i] >= low) hits[atomicAdd(&S.hits, 1u)] = static_cast<uint16_t>(i);
+      if (tops[i] > -INFINITY && tops[i] + 3.0f * slack(S.off[i / C].h, tops[i]) >= t)
+        hits[atomicAdd(&S.hits, 1u)] = static_cast<uint16_t>(i);
     __syncthreads();
   };
   // The vectors of hit slice i.
@@ -607,8 +628,8 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
 #pragma unroll
         for (int e = 0; e < kPer; ++e) top = fmaxf(top, x[e]);
       }
-      S.lanes[i * 32 + lane] = top > -INFINITY && top >= S.m[w] - kFar ? S.off[w].h + (top - S.m[w])
-                                                                        : -INFINITY;
+      S.lanes[i * 32 + lane] = top > -INFINITY && top >= S.m[w] - kFar
+                                   ? at_least(S.off[w].h, top - S.m[w]) : -INFINITY;
     }
     __syncthreads();
     least = nth_bound(S, S.lanes, few * 32, n_out, best, &have);

@@ -1,5 +1,5 @@
 """pkv.beam_select's order where sums' roundings could change it: equal beams at any place in
-memory."""
+memory, scores that cancel logits' gaps."""
 
 import math
 
@@ -72,3 +72,26 @@ def test_flat_equal_beams_wherever_their_rows_begin(dt):
         x = row.repeat(per, 1)
         scores = -torch.rand(1, 1, generator=g).expand(1, per).contiguous() * 5
         check(x, x.to(DEV), scores, 2 * per, eos=int(row.argmax()))
+
+
+# ------------------------------------------------------------------ scores that cancel
+
+
+@pytest.mark.parametrize("size", [1e3, 1e4, 1e5, 1e6, 1e8])
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+def test_scores_that_cancel_a_gap_of_the_logits(size, dt):
+    """One logit is far above the others and the score as far above zero: but for the first,
+    candidates are small numbers that are differences of large ones."""
+    size = float(torch.tensor(size).to(dt))
+    g = torch.Generator().manual_seed(3)
+    for trial in range(8):
+        v = 20000 + 3 * trial
+        x = torch.randn(3, v, generator=g).to(dt)
+        x[0, 17 * trial] = size
+        x[2, 40 + trial] = size / 2
+        one = torch.tensor([[size]])
+        check(x[:1], x[:1].to(DEV), one, 4)
+        check(x[:1], x[:1].to(DEV), one, 40, eos=3)
+        scores = torch.tensor([[size, 9.0, size / 2]])
+        for n in (2, 4, 40):
+            check(x, x.to(DEV), scores, n, eos=5)
