@@ -617,9 +617,11 @@ int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dtype dt, int 
  * score s = scores[b, w] offers for each token v the candidate
  *   t(w, v) = s + logits[b * W + w, v] - ln sum_u exp(logits[b * W + w, u]),
  * but for tokens whose logit is -inf or more than 2^126 below the beam's largest.
- * A beam whose score is -inf is dead and offers nothing, whatever its logits.  Candidates are ordered by t as a real
- * number, equal ones by (w, v): where the sums' rounding leaves the order of two
- * candidates open, their sums are taken again to some 2^-36.
+ * A beam whose score is -inf is dead and offers nothing, whatever its logits.
+ * Candidates are ordered by t as a real number, equal ones by (w, v): where the sums'
+ * rounding leaves the order of two candidates open, their logarithms are taken again
+ * to some 2^-36, and scores and logits count with all their bits.  The logarithms
+ * that then decide do not depend on where rows lie: equal rows have equal ones.
  *   - out_parents / out_tokens / out_scores [B, n_out]: the n_out best candidates
  *     with v != eos, best first; -1, -1 and -inf where there are no more;
  *   - ended [B, W] (or NULL): t(w, eos) where fewer than n_out candidates of the
@@ -628,7 +630,8 @@ int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dtype dt, int 
  * that is NaN or outside +-2^126, or a NaN or +inf among its logits, sets
  * PKV_ST_NONFINITE and offers nothing; one whose logits are all -inf sets
  * PKV_ST_ALL_NEG_INF and offers nothing.  Scores are off by less than
- * 3e-6 (the sum's logarithm) and one rounding to fp32.
+ * 3e-6 (the sum's logarithm), some 2^-46 of the beam's score and of the logit's
+ * distance from the largest, and one rounding to fp32.
  *   logits [B * W, V] of type dt (fp32 or bf16), row_stride in elements, rows may
  *   begin anywhere; scores [B, W] fp32; status device int32 or NULL; workspace of
  *   pkv_beam_select_workspace_bytes(...) bytes, 16-byte aligned, of any contents;

@@ -15,10 +15,12 @@
 // way from a logit to the slice's maximum add up to theirs, whose mean under the
 // slice's weights is at most log2 of its elements, 11: 1.0e-6.  Three exponentials on
 // that way are off by 2^-22 each, the sum by some 11 + 5 + 4 roundings of 2^-24.  A row's
-// log-sum-exp is therefore off by less than 2.9e-6, the difference of two by less than
-// kNear; joining the slices (sums of two fp32 values) adds nothing to speak of.
-// Candidates of different rows that lie nearer than kNear and could change the result
-// make the CTA sum their rows again (exp_below), to some 2^-36.  Candidates of one row
+// log-sum-exp is therefore off by less than 3e-6 (1.02 + 0.72 + 1.19), the difference of
+// two by less than kNear; joining the slices (sums of two fp32 values) adds nothing to
+// speak of.  Candidates of different rows that lie nearer than kNear and could change the
+// result make the CTA sum their rows again (exp_below), to some 2^-36, and compare them by
+// all bits of t (make_words): equal rows, and rows that differ by a constant, tie where the
+// numbers are equal, and a score far from zero hides nothing.  Candidates of one row
 // go by their logits and need no sums.  No fp64: this part has a 64th of its rate.
 //
 // Bound: the logits' bytes; with few rows the chain of loads and barriers.
@@ -50,6 +52,7 @@ constexpr int kThreads = 512;        // of the second kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostSlices = 288;     // of a row; 9 a lane
 constexpr int kCand = 1024;          // candidates it can rank at once, endings apart
+constexpr int kWords = 9;            // of a number in units of 2^-149: 2^129 is bit 278
 constexpr int kBins = 1024;
 constexpr float kBinsPerNat = 16.0f;
 constexpr float kNear = 6e-6f;
@@ -282,15 +285,18 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 4) beam_stream_kernel(
 }
 
 struct Shared {
-  FF off[PKV_MAX_BEAMS];         // score - ln sum_u exp(x_u - m): t is this plus x - m
+  FF log[PKV_MAX_BEAMS];         // ln sum_u exp(x_u - m)
+  FF off[PKV_MAX_BEAMS];         // score less that: t is this plus x - m
+  float score[PKV_MAX_BEAMS];
   float xmin[PKV_MAX_BEAMS];     // logits from here on are candidates
   float m[PKV_MAX_BEAMS];        // largest logit, the ending's among them
   float x_end[PKV_MAX_BEAMS];    // the ending's
   int live[PKV_MAX_BEAMS];
   unsigned long long key[kCand + PKV_MAX_BEAMS];   // falls as t does
-  unsigned long long rest[kCand + PKV_MAX_BEAMS];  // order of equal ones, ascending
+  unsigned long long rest[kCand + PKV_MAX_BEAMS];  // order of equal ones and in a beam, ascending
   float x[kCand + PKV_MAX_BEAMS];
   uint32_t id[kCand + PKV_MAX_BEAMS];              // kEnd | w << 20 | v
+  uint32_t words[kWords][kCand + PKV_MAX_BEAMS];   // t by all its bits, rises as t does
   int rank[kCand + PKV_MAX_BEAMS];
   float lanes[PKV_MAX_BEAMS * 32];                 // largest of the lanes of few slices
   NthScratch<kThreads> nth;
@@ -418,17 +424,66 @@ __device__ __forceinline__ void make_keys(Shared& S, int i, float best) {
               static_cast<unsigned long long>(~float_key(S.x[i])) << 20 | token_of(id);
 }
 
+// w += x, in two's complement and units of 2^-149.
+__device__ __forceinline__ void add_bits(uint32_t (&w)[kWords], float x) {
+  const uint32_t u = __float_as_uint(x), e = (u >> 23) & 255u;
+  const unsigned long long m = (u & 0x7fffffu) | (e != 0u ? 0x800000u : 0u);
+  const int shift = static_cast<int>(max(e, 1u)) - 1, at = shift >> 5;
+  const unsigned long long part = m << (shift & 31);
+  const bool minus = (u >> 31) != 0u;
+  uint32_t carry = minus ? 1u : 0u;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    uint32_t a = k == at ? static_cast<uint32_t>(part) : k == at + 1 ? static_cast<uint32_t>(part >> 32) : 0u;
+    if (minus) a = ~a;
+    const unsigned long long sum = static_cast<unsigned long long>(w[k]) + a + carry;
+    w[k] = static_cast<uint32_t>(sum);
+    carry = static_cast<uint32_t>(sum >> 32);
+  }
+}
+
+// Candidate i's t = score + x - m - log by all its bits: exact but for log itself.
+__device__ __forceinline__ void make_words(Shared& S, int i) {
+  const int b = beam_of(S.id[i]);
+  uint32_t w[kWords] = {};
+  add_bits(w, S.score[b]);
+  add_bits(w, S.x[i]);
+  add_bits(w, -S.m[b]);
+  add_bits(w, -S.log[b].h);
+  add_bits(w, -S.log[b].l);
+  w[kWords - 1] ^= 0x80000000u;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) S.words[k][i] = w[k];
+}
+
+// Whether candidate i comes before j of another beam, by their words and then by beam.
+__device__ __forceinline__ bool before(const Shared& S, int i, int j) {
+#pragma unroll 1
+  for (int k = kWords - 1; k >= 0; --k) {
+    const uint32_t a = S.words[k][i], b = S.words[k][j];
+    if (a != b) return a > b;
+  }
+  return S.rest[i] < S.rest[j];
+}
+
 // The places of c candidates: among those that go on, of an ending among all.  A warp a
-// candidate.  NEAR: rows whose candidates are near one another where that may matter
-// are left in S.near.
-template <bool NEAR>
-__device__ void rank_all(Shared& S, int c, int n_out) {
+// candidate.  Those of one beam go by their logits, those of two by their keys, but where
+// these are nearer than their errors (the sums', and the pairs' roundings at the size of
+// score, t and best): then, EXACT, by their words; else the rows of those that it may
+// matter for are left in S.near.
+template <bool EXACT>
+__device__ void rank_all(Shared& S, int c, int n_out, float best) {
   const int lane = threadIdx.x & 31;
+  auto rounding = [&](uint32_t id, unsigned long long key) {
+    return 0x1p-43f * (fabsf(S.off[beam_of(id)].h) + fabsf(best)) +
+           0x1p-43f * fabsf(key_float(static_cast<uint32_t>(key >> 32)));
+  };
 #pragma unroll 1
   for (int i = threadIdx.x >> 5; i < c; i += kWarps) {
     const unsigned long long key = S.key[i], rest = S.rest[i];
     const uint32_t id = S.id[i];
     const bool ending = (id & kEnd) != 0u;
+    const float near_i = kNear + rounding(id, key);
     int better = 0, close = 0;
     unsigned long long rows = 0ull;
 #pragma unroll 1
@@ -439,22 +494,25 @@ __device__ void rank_all(Shared& S, int c, int n_out) {
         const unsigned long long other = S.key[j];
         const uint32_t jd = S.id[j];
         const bool counts = ending || (jd & kEnd) == 0u;
-        is_better = counts && (other > key || (other == key && S.rest[j] < rest));
-        if (NEAR && beam_of(jd) != beam_of(id)) {
+        if (beam_of(jd) == beam_of(id)) {
+          is_better = S.rest[j] < rest;
+        } else {
           const float d = (key_float(static_cast<uint32_t>(other >> 32)) -
                            key_float(static_cast<uint32_t>(key >> 32))) +
                           (key_float(static_cast<uint32_t>(other)) - key_float(static_cast<uint32_t>(key)));
-          is_near = fabsf(d) <= kNear;
-          if (is_near) rows |= 1ull << beam_of(jd) | 1ull << beam_of(id);
-          is_near = is_near && counts;
+          is_near = fabsf(d) <= near_i + rounding(jd, other);
+          if (!EXACT && is_near) rows |= 1ull << beam_of(jd) | 1ull << beam_of(id);
+          is_better = EXACT && is_near ? before(S, j, i) : other > key;
         }
+        is_better = is_better && counts;
+        is_near = is_near && counts;
       }
       better += __popc(__ballot_sync(kFull, is_better));
-      if (NEAR) close += __popc(__ballot_sync(kFull, is_near));
+      if (!EXACT) close += __popc(__ballot_sync(kFull, is_near));
     }
     if (lane == 0) S.rank[i] = better;
     // (A candidate that no exchange brings among the best matters to nobody.)
-    if (NEAR && rows != 0ull && better - close < n_out) atomicOr(&S.near, rows);
+    if (!EXACT && rows != 0ull && better - close < n_out) atomicOr(&S.near, rows);
   }
 }
 
@@ -554,14 +612,14 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
     }
     const bool bad = score != -INFINITY && (!(fabsf(score) <= kFar) || !(m < INFINITY));
     const bool live = score != -INFINITY && !bad && m > -INFINITY;
-    FF off = {0.0f, 0.0f};
+    FF off = {0.0f, 0.0f}, log = off;
     if (live) {
       FF sum = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < kOwn; ++i)
         if (i * 32 < C && i * 32 + lane < C) sum = add(sum, mul(exp_below(part[i].x, m), part[i].y));
-      sum = log_of(warp_sum(sum));
-      off = add(FF{-sum.h, -sum.l}, score);
+      log = log_of(warp_sum(sum));
+      off = add(FF{-log.h, -log.l}, score);
     }
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
@@ -572,7 +630,9 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
       S.m[w] = m;
       S.x_end[w] = x_end;
       S.live[w] = live;
+      S.log[w] = log;
       S.off[w] = off;
+      S.score[w] = score;
       if (bad) atomicOr(&S.flag, PKV_ST_NONFINITE);
       else if (score != -INFINITY && !live) atomicOr(&S.flag, PKV_ST_ALL_NEG_INF);
     }
@@ -672,8 +732,11 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
   const bool many = S.count > kCand;
   __syncthreads();
   auto refine = [&](int w) {
-    const FF sum = log_of(exact_sum<T>(P, S, static_cast<int>(row0) + w, S.m[w]));
-    if (tid == 0) S.off[w] = add(FF{-sum.h, -sum.l}, P.scores[row0 + w]);
+    const FF log = log_of(exact_sum<T>(P, S, static_cast<int>(row0) + w, S.m[w]));
+    if (tid == 0) {
+      S.log[w] = log;
+      S.off[w] = add(FF{-log.h, -log.l}, S.score[w]);
+    }
     __syncthreads();
   };
   if (many) {
@@ -687,9 +750,12 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
       refine(w);
       row_best<T>(P, S, w, static_cast<int>(row0) + w);
       const int c = static_cast<int>(S.count);  // at most 2 n_out
-      if (tid < c) make_keys(S, tid, best);
+      if (tid < c) {
+        make_keys(S, tid, best);
+        make_words(S, tid);
+      }
       __syncthreads();
-      rank_all<false>(S, c, n_out);
+      rank_all<true>(S, c, n_out, best);
       __syncthreads();
       int to = n_out;
       float x = 0.0f;
@@ -723,10 +789,14 @@ __global__ void __launch_bounds__(kThreads) beam_finish_kernel(const __grid_cons
   // ---- ranks, again where the sums' errors leave them open
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    for (int i = tid; i < c; i += kThreads) make_keys(S, i, best);
+    const bool exact = pass > 0 || many;
+    for (int i = tid; i < c; i += kThreads) {
+      make_keys(S, i, best);
+      if (exact) make_words(S, i);
+    }
     __syncthreads();
-    if (pass == 0 && !many) rank_all<true>(S, c, n_out);
-    else rank_all<false>(S, c, n_out);
+    if (exact) rank_all<true>(S, c, n_out, best);
+    else rank_all<false>(S, c, n_out, best);
     __syncthreads();
     const unsigned long long again = pass == 0 ? S.near : 0ull;
     if (again == 0ull) break;

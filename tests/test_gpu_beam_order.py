@@ -1,7 +1,9 @@
 """pkv.beam_select's order where sums' roundings could change it: equal beams at any place in
-memory, scores that cancel logits' gaps."""
+memory, scores that cancel logits' gaps, equal candidates of beams with other scores, scores
+far from zero."""
 
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -95,3 +97,66 @@ def test_scores_that_cancel_a_gap_of_the_logits(size, dt):
         scores = torch.tensor([[size, 9.0, size / 2]])
         for n in (2, 4, 40):
             check(x, x.to(DEV), scores, n, eos=5)
+
+
+# ------------------------------------------------------------------ the order of real numbers
+
+
+def exact_select(x, scores, n):
+    """The definition by whole fractions, all but the sums' logarithm (fp64)."""
+    b, w = scores.shape
+    parents = torch.full((b, n), -1, dtype=torch.int32)
+    tokens, out = parents.clone(), torch.full((b, n), -math.inf, dtype=torch.float64)
+    least = math.inf  # difference of two candidates that are not equal
+    for i in range(b):
+        cand = []
+        for j in range(w):
+            row = x[i * w + j].double()
+            m = float(row.max())
+            log = Fraction(math.log(math.fsum(torch.exp(row - m).tolist())))
+            base = Fraction(float(scores[i, j])) - Fraction(m) - log
+            edge = float(row.topk(min(n, row.numel())).values[-1])
+            cand += [(-(base + Fraction(float(row[t]))), j, t)
+                     for t in (row >= edge).nonzero().flatten().tolist()]
+        cand.sort()
+        for k, (t, j, v) in enumerate(cand[:n]):
+            parents[i, k], tokens[i, k], out[i, k] = j, v, float(-t)
+            if k and t != cand[k - 1][0]:
+                least = min(least, float(t - cand[k - 1][0]))
+    return (parents, tokens, out, None), least
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("far", [0.0, -2048.0, 2.0 ** 20])
+def test_equal_candidates_of_beams_with_other_scores(far, dt):
+    """Beams with the same logits, multiples of 1/8 as the scores are: a lower score meets a
+    higher logit, and the two candidates are the same number."""
+    g = torch.Generator().manual_seed(4)
+    b, w, v = 800, 4, 50
+    x = (torch.randint(-40, 41, (b, 1, v), generator=g) / 8).expand(b, w, v).reshape(b * w, v).to(dt)
+    scores = far - torch.randint(0, 16, (b, w), generator=g) / 8
+    for n in (8, 32):
+        want, least = exact_select(x, scores, n)
+        assert least >= 0.125
+        check(x, x.to(DEV), scores, n, want)
+
+
+@pytest.mark.parametrize("flat", [False, True])
+@pytest.mark.parametrize("score", [-2.0 ** 20, -2.0 ** 27, 2.0 ** 30, -1e9, 1e30])
+def test_near_candidates_of_beams_with_far_scores(score, flat):
+    """Logits a step of fp32 apart under scores whose own steps are much larger."""
+    g = torch.Generator().manual_seed(5)
+    for trial in range(6):
+        v = 3001 + 2 * trial
+        row = -torch.rand(v, generator=g)
+        if flat:  # more candidates than the list holds
+            row[100:1900] = 1.0
+        # The second beam's are the first's in another order, its largest half a step higher.
+        row[:24] = 1.0 + torch.randperm(24, generator=g) * 2.0 ** -22
+        x = torch.stack([row, row])
+        x[1, :24] += 2.0 ** -23
+        x[1] = x[1, torch.randperm(v, generator=g)]
+        scores = torch.tensor([[score, score]])
+        want, least = exact_select(x, scores, 30)
+        assert least > 1e-10
+        check(x, x.to(DEV), scores, 30, want)
