@@ -69,7 +69,7 @@ struct SelectParams {
   int32_t* pages;         // [n_tokens, kv_heads, budget]
   int32_t* lengths;       // [n_tokens]
   int2* where;            // workspace: [n_tokens] table row, position or -1
-  float* sums;            // workspace: [n_tokens, kv_heads] Cell::sums
+  float2* sums;           // workspace: [n_tokens, kv_heads] Cell::sums and unit
   float2* score;          // workspace: [n_tokens, kv_heads, most]: score, scale
   double* exact;          // workspace: the same shape
   int most;               // pages of a table row
@@ -104,10 +104,13 @@ __device__ __forceinline__ int page_at(const AttendParams& A, int row, int b) {
                           static_cast<int64_t>(b) * A.c.page_size));
 }
 
-// A page's score to some 2^-46 of its terms: one warp, all lanes get it.  Lanes share a
-// query head's dimensions, as few as the heads allow: the sums' chains are what it waits for.
+// A page's score times `unit` (measure_queries), to some 2^-46 of its terms: one warp, all
+// lanes get it.  The power of two keeps products of queries at the ends of their range
+// within fp32's.  Lanes share a query head's dimensions, as few as the heads allow: the
+// sums' chains are what it waits for.
 template <typename T>
-__device__ double exact_score(const SelectParams& P, const uint16_t* q, int row, int h, int b) {
+__device__ double exact_score(const SelectParams& P, const uint16_t* q, float unit, int row, int h,
+                              int b) {
   const AttendParams& A = P.a;
   const int lane = threadIdx.x & 31;
   const int page = page_at(A, row, b);
@@ -128,7 +131,8 @@ __device__ double exact_score(const SelectParams& P, const uint16_t* q, int row,
         const float2 l1 = Pair<__half>::unpack(e4m3x2_to_f16x2(lo >> 16));
         const float2 h0 = Pair<__half>::unpack(e4m3x2_to_f16x2(hi));
         const float2 h1 = Pair<__half>::unpack(e4m3x2_to_f16x2(hi >> 16));
-        const float2 a = Pair<T>::unpack(x.x), z = Pair<T>::unpack(x.y);
+        float2 a = Pair<T>::unpack(x.x), z = Pair<T>::unpack(x.y);
+        a.x *= unit, a.y *= unit, z.x *= unit, z.y *= unit;
         const FF u = two_sum(fmaxf(a.x * l0.x, a.x * h0.x), fmaxf(a.y * l0.y, a.y * h0.y));
         const FF v = two_sum(fmaxf(z.x * l1.x, z.x * h1.x), fmaxf(z.y * l1.y, z.y * h1.y));
         s = add(s, add(u, v));
@@ -161,7 +165,7 @@ struct Cell {
   float sums;         // largest sum of magnitudes of a query, scaled
 };
 
-// Queries' largest element and sum, by one warp.
+// Queries' largest element and sum, by one warp: c's unit and sums.
 template <typename T>
 __device__ __forceinline__ void measure_queries(const SelectParams& P, Cell& c) {
   const AttendParams& A = P.a;
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     if (j < A.n_tokens && c.count > P.budget && b0 < end) {
       c.q = A.q + j * A.q_ts + static_cast<int64_t>(c.h) * A.group * A.q_hs;
       score_pages<T, KW>(P, c, b0, end, P.score + (j * heads + c.h) * P.most, ring);
-      if (t0 == 0 && lane == 0) __stcg(P.sums + j * heads + c.h, c.sums);
+      if (t0 == 0 && lane == 0) __stcg(P.sums + j * heads + c.h, make_float2(c.sums, c.unit));
     }
     left -= take;
     if (left <= 0) break;
@@ -647,7 +651,7 @@ __device__ void pick_pages(const SelectParams& P, PickShared<THREADS>& S, const 
         const int l = __ffs(todo) - 1;
         todo &= todo - 1u;
         const float x = __shfl_sync(kFull, s, l);
-        const double y = x == INFINITY ? INFINITY : exact_score<T>(P, c.q, c.row, c.h, w + l);
+        const double y = x == INFINITY ? INFINITY : exact_score<T>(P, c.q, c.unit, c.row, c.h, w + l);
         if (lane == 0) {
           exact[w + l] = y;
           const int i = atomicAdd(&S.few, 1);
@@ -738,7 +742,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const __grid_constant__ S
   launch_dependents();
   grid_dependency_wait();
   const int2 w = __ldcg(P.where + j);
-  const float sums = __ldcg(P.sums + cell);  // (not written where nothing was scored)
+  const float2 sums = __ldcg(P.sums + cell);  // (not written where nothing was scored)
   Cell c;
   c.h = static_cast<int>(cell - static_cast<int64_t>(j) * A.c.kv_heads);
   c.row = w.x;
@@ -753,7 +757,8 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const __grid_constant__ S
     return;
   }
   c.q = A.q + j * A.q_ts + static_cast<int64_t>(c.h) * A.group * A.q_hs;
-  c.sums = sums;
+  c.sums = sums.x;
+  c.unit = sums.y;
   pick_pages<T, THREADS>(P, S, c, P.score + cell * P.most, P.exact + cell * P.most, out);
 }
 
@@ -794,7 +799,7 @@ extern "C" size_t pkv_select_pages_workspace_bytes(int64_t n_tokens, int kv_head
       pt_cols < 1 || pt_cols > (int64_t{1} << 30) || page_size < 1)
     return 0;
   const int64_t cells = n_tokens * kv_heads * div_ceil(pt_cols, page_size);
-  return static_cast<size_t>(round16(n_tokens * 8) + round16(n_tokens * kv_heads * 4) + 16 * cells);
+  return static_cast<size_t>(round16(n_tokens * 8) + round16(n_tokens * kv_heads * 8) + 16 * cells);
 }
 
 extern "C" int pkv_select_pages(const pkv_kv_cache* cache, const void* bounds, const void* q,
@@ -865,8 +870,8 @@ extern "C" int pkv_select_pages(const pkv_kv_cache* cache, const void* bounds, c
   uint8_t* at = static_cast<uint8_t*>(workspace);
   P.where = reinterpret_cast<int2*>(at);
   at += round16(n_tokens * 8);
-  P.sums = reinterpret_cast<float*>(at);
-  at += round16(n_tokens * cache->kv_heads * 4);
+  P.sums = reinterpret_cast<float2*>(at);
+  at += round16(n_tokens * cache->kv_heads * 8);
   P.score = reinterpret_cast<float2*>(at);
   P.exact = reinterpret_cast<double*>(at + 8 * cells);
   P.budget = budget, P.sink = sink, P.recent = recent;
