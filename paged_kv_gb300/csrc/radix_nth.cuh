@@ -39,8 +39,9 @@ __device__ uint32_t nth_key(NthScratch<THREADS>& S, uint32_t n, uint32_t* count,
       if (key != 0u && (key & above) == prefix) atomicAdd(&S.bins[(key >> shift) & mask], 1u);
     });
     __syncthreads();
-    // Thread t's bins, from the top: kBins - 1 - 4 t and the three below.
+    // Thread t's bins, from the top: kBins - 1 - t kOwn and the kOwn - 1 below.
     constexpr int kOwn = kBins / THREADS;
+    static_assert(kOwn * THREADS == kBins, "every bin is a thread's");
     uint32_t own = 0;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) own += S.bins[kBins - 1 - tid * kOwn - i];
