@@ -804,7 +804,11 @@ int pkv_update_bounds(const pkv_kv_cache* cache, void* bounds, const int32_t* ou
  *   elements; bounds as for pkv_update_bounds; cached_len, device_len, table_idx
  *   [B] int32; page_table [pt_rows, pt_cols] int32; status device int32 or NULL;
  *   workspace of pkv_select_pages_workspace_bytes(...) bytes, 16-byte aligned, of
- *   any contents; no two calls that may overlap share one.
+ *   any contents; no two calls that may overlap share one.  It has 8 bytes for every
+ *   token, head and page of a table row (pt_cols / page_size, whatever the lengths)
+ *   and 8 for every token and head: 16 tokens, 8 heads, rows of 36864 positions in
+ *   pages of 16: 2.4 MB; 4096 tokens of these: 604 MB.  Calls of fewer tokens, or a
+ *   table whose rows are as long as the requests need, take less.
  * Errors: those of pkv_paged_attention's arguments, and PKV_EINVAL for n_tokens
  * outside [0, PKV_MAX_SPARSE_TOKENS], budget outside [1, 65536], sink < 0,
  * recent < 1 or sink + recent > budget.  B == 0 or n_tokens == 0 is a no-op.

@@ -70,8 +70,8 @@ struct SelectParams {
   int32_t* lengths;       // [n_tokens]
   int2* where;            // workspace: [n_tokens] table row, position or -1
   float2* sums;           // workspace: [n_tokens, kv_heads] Cell::sums and unit
-  float2* score;          // workspace: [n_tokens, kv_heads, most]: score, scale
-  double* exact;          // workspace: the same shape
+  float2* score;          // workspace: [n_tokens, kv_heads, most]: score and scale, then, where
+                          // sums are in doubt, a page's place in the order
   int most;               // pages of a table row
   int budget, sink, recent;
 };
@@ -149,12 +149,14 @@ __device__ double exact_score(const SelectParams& P, const uint16_t* q, float un
   return best * static_cast<double>(A.c.k_scale[at]);
 }
 
-// An order of doubles as whole numbers; never 0.
+// An order of doubles as whole numbers; never 0 or kSure.
 __device__ __forceinline__ unsigned long long double_key(double x) {
   const long long b = __double_as_longlong(x + 0.0);
   return static_cast<unsigned long long>(b) ^
          (static_cast<unsigned long long>(b >> 63) | 0x8000000000000000ull);
 }
+
+constexpr unsigned long long kSure = ~0ull;  // above all of those
 
 // What a warp of the CTA knows of its (token, head).
 struct Cell {
@@ -497,7 +499,7 @@ struct PickShared {
 // Lists a cell's pages, by one CTA, whose warps have neighbouring pages each.
 template <typename T, int THREADS>
 __device__ void pick_pages(const SelectParams& P, PickShared<THREADS>& S, const Cell& c,
-                           const float2* score, double* exact, int32_t* out) {
+                           float2* score, int32_t* out) {
   constexpr int kWarps = THREADS / 32;
   const AttendParams& A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -610,16 +612,23 @@ __device__ void pick_pages(const SelectParams& P, PickShared<THREADS>& S, const 
     // Each score, and so the k-th largest, is off by at most half of this.
     e = 2.0f * (0x1p-17f * 448.0f * kDown) * c.sums * scale;
   }
+  // With sums taken again, their order by whole numbers in the scores' places: 0 for a page
+  // that is not taken and kSure for one that is, but where scores are held those in doubt
+  // alone have one.
+  unsigned long long* const keys = reinterpret_cast<unsigned long long*>(score);
+  auto key_of = [&](int b) { return held && !in_doubt(at(b)) ? 0ull : __ldcg(keys + b); };
   // 0: not taken, 1: taken, 2: in doubt; with `again`: equal to the last one taken
   unsigned long long nth = 0;
   auto kind = [&](int b, bool again) {
     if (b >= c.count) return 0;
     if (b < m0 || b >= m1) return 1;
     if (k == 0) return 0;
-    const float s = at(b);
-    if (!in_doubt(s)) return s > t ? 1 : 0;
-    if (!again) return 2;
-    const unsigned long long y = double_key(exact[b]);
+    if (!again || held) {
+      const float s = at(b);
+      if (!in_doubt(s)) return s > t ? 1 : 0;
+      if (!again) return 2;
+    }
+    const unsigned long long y = __ldcg(keys + b);
     return y > nth ? 1 : y == nth ? 2 : 0;
   };
   int2 before, all;  // sure ones, and those in doubt (or equal)
@@ -645,17 +654,21 @@ __device__ void pick_pages(const SelectParams& P, PickShared<THREADS>& S, const 
 #pragma unroll 1
     for (int w = w0; w < w1; w += 32) {
       const int b = w + lane;
-      const float s = b >= m0 && b < m1 ? at(b) : 0.0f;
-      unsigned todo = __ballot_sync(kFull, b >= m0 && b < m1 && in_doubt(s));
+      const bool competes = b >= m0 && b < m1;
+      const float s = competes ? at(b) : 0.0f;
+      const bool doubt = competes && in_doubt(s);
+      unsigned todo = __ballot_sync(kFull, doubt);  // (all have read their scores)
+      if (!held && competes && !doubt) keys[b] = s > t ? kSure : 0ull;
       while (todo != 0u) {
         const int l = __ffs(todo) - 1;
         todo &= todo - 1u;
         const float x = __shfl_sync(kFull, s, l);
         const double y = x == INFINITY ? INFINITY : exact_score<T>(P, c.q, c.unit, c.row, c.h, w + l);
         if (lane == 0) {
-          exact[w + l] = y;
+          const unsigned long long key = double_key(y);
+          keys[w + l] = key;
           const int i = atomicAdd(&S.few, 1);
-          if (i < kFew) S.key[i] = double_key(y);
+          if (i < kFew) S.key[i] = key;
         }
       }
     }
@@ -681,19 +694,17 @@ __device__ void pick_pages(const SelectParams& P, PickShared<THREADS>& S, const 
       // The upper halves' n-th largest, then that of the lower halves beside it.
       uint32_t n;
       const uint32_t up = nth_key<THREADS, 3>(S.nth, places, &n, [&](auto&& f) {
-        for (int b = b0; b < b1; b += 32)
-          f(in_doubt(at(b)) ? static_cast<uint32_t>(double_key(exact[b]) >> 32) : 0u);
+        for (int b = b0; b < b1; b += 32) {
+          const unsigned long long y = key_of(b);
+          f(y == kSure ? 0u : static_cast<uint32_t>(y >> 32));
+        }
       });
       const int rest = static_cast<int>(S.nth.left);
       __syncthreads();
       const uint32_t low = nth_key<THREADS, 3>(S.nth, rest, &n, [&](auto&& f) {
         for (int b = b0; b < b1; b += 32) {
-          uint32_t x = 0u;
-          if (in_doubt(at(b))) {
-            const unsigned long long y = double_key(exact[b]);
-            if (static_cast<uint32_t>(y >> 32) == up) x = static_cast<uint32_t>(y);
-          }
-          f(x);
+          const unsigned long long y = key_of(b);
+          f(y != kSure && static_cast<uint32_t>(y >> 32) == up ? static_cast<uint32_t>(y) : 0u);
         }
       });
       // (0 where fewer than `rest` are above 0: it is one of those that are 0.)
@@ -759,7 +770,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const __grid_constant__ S
   c.q = A.q + j * A.q_ts + static_cast<int64_t>(c.h) * A.group * A.q_hs;
   c.sums = sums.x;
   c.unit = sums.y;
-  pick_pages<T, THREADS>(P, S, c, P.score + cell * P.most, P.exact + cell * P.most, out);
+  pick_pages<T, THREADS>(P, S, c, P.score + cell * P.most, out);
 }
 
 template <typename T, int KW>
@@ -799,7 +810,7 @@ extern "C" size_t pkv_select_pages_workspace_bytes(int64_t n_tokens, int kv_head
       pt_cols < 1 || pt_cols > (int64_t{1} << 30) || page_size < 1)
     return 0;
   const int64_t cells = n_tokens * kv_heads * div_ceil(pt_cols, page_size);
-  return static_cast<size_t>(round16(n_tokens * 8) + round16(n_tokens * kv_heads * 8) + 16 * cells);
+  return static_cast<size_t>(round16(n_tokens * 8) + round16(n_tokens * kv_heads * 8) + 8 * cells);
 }
 
 extern "C" int pkv_select_pages(const pkv_kv_cache* cache, const void* bounds, const void* q,
@@ -866,14 +877,12 @@ extern "C" int pkv_select_pages(const pkv_kv_cache* cache, const void* bounds, c
   P.pages = pages;
   P.lengths = out_lengths;
   P.most = static_cast<int>(div_ceil(pt_cols, cache->page_size));
-  const int64_t cells = n_tokens * cache->kv_heads * P.most;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   P.where = reinterpret_cast<int2*>(at);
   at += round16(n_tokens * 8);
   P.sums = reinterpret_cast<float2*>(at);
   at += round16(n_tokens * cache->kv_heads * 8);
   P.score = reinterpret_cast<float2*>(at);
-  P.exact = reinterpret_cast<double*>(at + 8 * cells);
   P.budget = budget, P.sink = sink, P.recent = recent;
   if (n_tokens * cache->kv_heads > INT32_MAX)
     return fail(PKV_EINVAL, "%lld tokens of %d heads are too many", (long long)n_tokens,
