@@ -626,7 +626,8 @@ int pkv_adjust_logits(const void* logits, int64_t row_stride, pkv_dtype dt, int 
  *     with v != eos, best first; -1, -1 and -inf where there are no more;
  *   - ended [B, W] (or NULL): t(w, eos) where fewer than n_out candidates of the
  *     request, endings among them, come before it, else -inf.
- * eos outside [0, V): no ending (ended is all -inf).  A live beam with a score
+ * eos outside [0, V): no ending (ended is all -inf); one token a call ends beams.
+ * A live beam with a score
  * that is NaN or outside +-2^126, or a NaN or +inf among its logits, sets
  * PKV_ST_NONFINITE and offers nothing; one whose logits are all -inf sets
  * PKV_ST_ALL_NEG_INF and offers nothing.  Scores are off by less than
@@ -673,9 +674,10 @@ size_t pkv_beam_select_workspace_bytes(int B, int W, int V, pkv_dtype dt);
  * those that no row holds.
  *
  * The rows in table_idx have to differ from one another, L positions of a
- * parent's row to lie in its pages, and no page of free_slots to be held by a row.  If the pages do not fit, PKV_ST_NOSPC is
- * set; if a parent lies outside [-1, W) or a row outside the table or the pool,
- * PKV_ST_ROW_OOB; if a parent's length lies outside [0, pt_cols], its last page
+ * parent's row to lie in its pages, and no page of free_slots to be held by a
+ * row.  If the pages do not fit, PKV_ST_NOSPC is set; if a parent lies outside
+ * [-1, W) or a row outside the table or the pool, PKV_ST_ROW_OOB; if a parent's
+ * length lies outside [0, pt_cols], its last page
  * would end past pt_cols, its tokens past the pool, or (with layers) a page to
  * copy lies outside the cache, PKV_ST_COL_OOB: then *total_out is 0 and nothing
  * else is written.
@@ -797,6 +799,7 @@ int pkv_update_bounds(const pkv_kv_cache* cache, void* bounds, const int32_t* ou
  *   outside the cache, too: PKV_ST_ROW_OOB);
  *   out_lengths [n_tokens] int32: positions in them, p's last: the same for all
  *   heads.
+ * Pages of all positions up to p compete: there is no first position and no window.
  * A token of a request that pkv_paged_attention refuses (its lengths, row or
  * number of tokens; the same status bits) gets -1 and 0, as does one past the
  * requests' tokens.

@@ -53,7 +53,8 @@ struct AttendParams {
   float scale_log2;            // sm_scale * log2(e)
   bool bf16;
   // Each token over pages of its own, for each cache head a list (attend_lists.cu and,
-  // in attend_units.cuh, LISTS): then a request is one token, and the lengths and the table are not used.
+  // in attend_units.cuh, LISTS): then a request is one token, and the lengths and the table
+  // are not used.
   const int32_t* lists;        // [B, c.kv_heads, budget] pages
   const int32_t* list_len;     // [B] positions in them
   int budget;

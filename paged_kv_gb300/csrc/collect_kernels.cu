@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 3) move_kernel(
   const int parts = static_cast<int>(div_ceil(P.pt_cols, kCols));
   const bool same = P.out_table == P.page_table;
   for (int64_t i = me; i < static_cast<int64_t>(P.B) * parts; i += warps) {
-    const int r = static_cast<int>(i / parts), c0 = static_cast<int>(i - static_cast<int64_t>(r) * parts) * kCols;
+    const int r = static_cast<int>(i / parts);
+    const int c0 = static_cast<int>(i - static_cast<int64_t>(r) * parts) * kCols;
     const int held = static_cast<int>(div_ceil(P.lengths[r], ps)) * ps;
     if (c0 >= held) continue;
     const int64_t row = static_cast<int64_t>(P.table_idx[r]) * P.pt_cols + c0;

@@ -9,7 +9,8 @@ namespace pkv {
 // it on the stream have ended or called launch_dependents().  Each of its blocks calls
 // grid_dependency_wait() before it touches memory and before it ends: then that kernel has
 // ended and what it wrote is seen, but by plain loads alone, not by the read-only path
-// (__ldg), whose data may not change while a kernel runs.  After anything but a kernel it is a plain launch.
+// (__ldg), whose data may not change while a kernel runs.  After anything but a kernel it
+// is a plain launch.
 template <class Kernel, class... A>
 cudaError_t launch_early(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
                          const A&... args) {

@@ -19,12 +19,13 @@
 // bounds a score's error, so the k-th largest true score lies within e_max of the
 // k-th largest score T, and only pages whose score is within e + e_max of T can be
 // taken or left wrongly.  Where there are more of those than places, their sums
-// are taken again as sums of two fp32 values (products of a query's 11 bits with a
-// code's 4 are exact in fp32).
+// are taken again as sums of two fp32 values (products of a query's 11 bits, scaled as
+// above, with a code's 4 are exact in fp32), and their places in the order stand where the
+// scores were.
 //
 // Bound: for many long requests the bounds' bytes, after 10 us of dependent loads (place,
 // page, bounds); for few tokens those chains.  64 requests of up to 32768, 8 heads of 128,
-// pages of 16: 59 us, of which the scores 40 (134 MB) and the choice the rest; one of
+// pages of 16: 59 us, of which the scores 40 (150 MB) and the choice the rest; one of
 // 36863: 18 us.
 
 #include <cuda_runtime.h>
